@@ -17,6 +17,10 @@ Functions (same names as the C entry points):
   mx8_dequantize(q, e8m0)              -> y f32 or bf16, q.shape
   mx8_dequant_reduce(qs, es)           -> y f32 or bf16, q.shape
   fp8q_quantize_tensorwise(x, fmt)     -> (q uint8 [n], scale f32 [1])
+
+The MoE layer's activation operators (norm into 8 bits, rows to their experts
+and back, their gradients) are those of ``layer.py``, over ``libfp8q_layer.so``
+and ``include/fp8q_layer.h``; they are names of this package too.
 """
 from __future__ import annotations
 
@@ -355,3 +359,9 @@ def fp8q_quantize_tensorwise(x: torch.Tensor, fmt: int = E4M3, q_out: Optional[t
     _run("fp8q_quantize_tensorwise", [x, q_out, scale_out], lib().fp8q_quantize_tensorwise,
          x.data_ptr(), n, _fmt(fmt), q_out.data_ptr(), scale_out.data_ptr(), _stream(x, stream), stream=stream)
     return q_out, scale_out
+
+
+from .layer import (RmsNorm, fp8q_moe_combine, fp8q_moe_combine_backward,  # noqa: E402,F401
+                    fp8q_moe_permute, fp8q_moe_sort, fp8q_moe_sort_workspace,
+                    fp8q_rms_norm_backward, fp8q_rms_norm_backward_workspace,
+                    fp8q_rms_norm_quantize, mx8_rms_norm_quantize)

@@ -1,4 +1,5 @@
-"""Build the HIP library ``libfp8q.so`` in-tree for gfx950 with hipcc.
+"""Build the HIP libraries ``libfp8q.so`` (the codec) and ``libfp8q_layer.so``
+(the MoE layer's activation operators) in-tree for gfx950 with hipcc.
 
     python -m dequantize_reduce_transfer_amd.build
 
@@ -30,8 +31,10 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB_PATH = os.path.join(PKG, "libfp8q.so")
+LAYER_LIB_PATH = os.path.join(PKG, "libfp8q_layer.so")
 
 SOURCES = ["quantize.hip", "dequant_reduce.hip", "mx8_quantize.hip", "api.hip"]
+LAYER_SOURCES = ["rms_norm.hip", "moe_sort.hip", "moe_rows.hip", "layer_api.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 CXXFLAGS = [
@@ -51,19 +54,26 @@ def _compile(src: str) -> str:
     return obj
 
 
-def build(verbose: bool = False) -> str:
-    """Compile every HIP source and link libfp8q.so (always rebuilds)."""
-    os.makedirs(BUILD_DIR, exist_ok=True)
-    with ThreadPoolExecutor(max_workers=min(len(SOURCES), os.cpu_count() or 1)) as ex:
-        objs = list(ex.map(_compile, SOURCES))
-    tmp = LIB_PATH + ".tmp%d" % os.getpid()
+def _link(objs, lib: str) -> None:
+    tmp = lib + ".tmp%d" % os.getpid()
     cmd = [HIPCC, "--offload-arch=" + ARCH, "-shared", "-fPIC", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError("link failed:\n%s\n%s" % (r.stdout, r.stderr))
-    os.replace(tmp, LIB_PATH)
+    os.replace(tmp, lib)
+
+
+def build(verbose: bool = False) -> str:
+    """Compile every HIP source and link both libraries (always rebuilds)."""
+    os.makedirs(BUILD_DIR, exist_ok=True)
+    sources = [*SOURCES, *LAYER_SOURCES]
+    with ThreadPoolExecutor(max_workers=min(len(sources), os.cpu_count() or 1)) as ex:
+        objs = list(ex.map(_compile, sources))
+    _link(objs[:len(SOURCES)], LIB_PATH)
+    _link(objs[len(SOURCES):], LAYER_LIB_PATH)
     if verbose:
         print("built", LIB_PATH)
+        print("built", LAYER_LIB_PATH)
     return LIB_PATH
 
 

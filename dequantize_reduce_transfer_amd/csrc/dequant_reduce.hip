@@ -27,6 +27,7 @@
 // only in registers.  The file also holds the MXFP8 receiver, which shares
 // this mapping, and the reduce -> requantize, which holds eight codes per
 // lane so that a block is one 16-lane row.
+#include "f32_encode.h"
 #include "fp8q_device.h"
 #include "launch.h"
 
@@ -631,37 +632,6 @@ hipError_t dispatch_k(int k, const PeerPtrs &P, uint64_t n, void *y, hipStream_t
 // under half the smallest FP8 subnormal, and the sequence keeps the
 // dividend's sign, so the code is the same signed zero.
 
-__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
-
-struct F32Scale {
-  float s;        // the stored scale (NaN for a non-finite block)
-  float sp;       // s * f
-  float rp;       // RN(1 / sp)
-  float f;        // 2^64 for blocks with amax below 2^-60, else 1
-  bool finite;
-};
-
-template <int FMT>
-__device__ __forceinline__ F32Scale f32_block_scale(uint32_t amax_bits) {
-  F32Scale r;
-  r.finite = amax_bits < 0x7F800000u;
-  const float s = scale_from_amax<FMT>(__uint_as_float(amax_bits));  // = IEEE amax / M
-  r.f = amax_bits < 0x21800000u ? 0x1p64f : 1.0f;          // amax < 2^-60
-  r.sp = s * r.f;
-  r.rp = recip_rn(r.sp);                                    // = IEEE 1 / sp
-  r.s = r.finite ? s : __uint_as_float(0x7FC00000u);
-  return r;
-}
-
-// SCALED = false may only be used where b.f == 1 (it skips x' = v * f).
-// The quotient goes to cvt4 with no clamp: |RN(v / s)| <= quotient_bound
-// for every v of a finite block (fp8q_device.h).
-template <int FMT, bool SCALED = true>
-__device__ __forceinline__ float f32_quot(float v, const F32Scale &b) {
-  const float xp = SCALED ? v * b.f : v;
-  return markstein_quotient(xp, b.sp, b.rp);
-}
-
 // Elements [start, n) (start is block-aligned): one block per pass, two
 // elements per lane, a whole-wave amax.
 template <int FIN, int FOUT, int K>
@@ -746,14 +716,6 @@ __device__ __forceinline__ void sum_tile8(const Tile8<K, U> &in, float (&acc)[U]
 #pragma unroll
       for (int j = 0; j < 8; ++j) acc[u][j] = (p == 0) ? v[j] : acc[u][j] + v[j];
     }
-}
-
-template <int FOUT, bool SCALED>
-__device__ __forceinline__ u32x2 quot8(const float (&a)[8], const F32Scale &sc) {
-  return u32x2{cvt4<FOUT>(f32_quot<FOUT, SCALED>(a[0], sc), f32_quot<FOUT, SCALED>(a[1], sc),
-                          f32_quot<FOUT, SCALED>(a[2], sc), f32_quot<FOUT, SCALED>(a[3], sc)),
-               cvt4<FOUT>(f32_quot<FOUT, SCALED>(a[4], sc), f32_quot<FOUT, SCALED>(a[5], sc),
-                          f32_quot<FOUT, SCALED>(a[6], sc), f32_quot<FOUT, SCALED>(a[7], sc))};
 }
 
 // One tile: sum, requantize, store the codes, and put the tile's 4U scales at
