@@ -78,7 +78,8 @@ fp8q_status norm_quantize(int out, const void *x, const void *residual, const vo
       overlaps_any(sr, {xr, rr, wr, tr}) || overlaps_any(tr, {xr, rr, wr}))
     return FP8Q_ERR_OVERLAP;
   const fp8q::NormForward a{x, residual, weight, weight_dtype == FP8Q_WEIGHT_BF16, eps,
-                            (uint32_t)hidden, rows, h_out, y_out, q_out, scales_out, rstd_out};
+                            (uint32_t)hidden, 1.0f / (float)hidden, rows, h_out, y_out, q_out,
+                            scales_out, rstd_out};
   return from_hip(fp8q::launch_rms_norm(out, a, static_cast<hipStream_t>(stream)));
 }
 
@@ -140,8 +141,8 @@ fp8q_status fp8q_rms_norm_backward(const void *dy_bf16, const void *h_bf16, cons
       overlaps_any(sr, {dyr, hr, wr, tr, dhr}))
     return FP8Q_ERR_OVERLAP;
   const fp8q::NormBackward a{dy_bf16, h_bf16, weight, weight_dtype == FP8Q_WEIGHT_BF16, rstd,
-                             dh_bf16, (uint32_t)hidden, rows, dx_out, dweight_out,
-                             static_cast<float *>(workspace)};
+                             dh_bf16, (uint32_t)hidden, 1.0f / (float)hidden, rows, dx_out,
+                             dweight_out, static_cast<float *>(workspace)};
   return from_hip(fp8q::launch_rms_norm_backward(a, static_cast<hipStream_t>(stream)));
 }
 

@@ -18,8 +18,11 @@ namespace fp8q {
 #ifndef FP8Q_LAYER_MAX_WAVES
 #define FP8Q_LAYER_MAX_WAVES (1ull << 24)
 #endif
+constexpr uint64_t max_workgroups(uint32_t waves) {
+  return FP8Q_LAYER_MAX_WAVES < waves ? 1 : FP8Q_LAYER_MAX_WAVES / waves;
+}
 inline uint32_t grid_for(uint64_t units, uint32_t per, uint32_t waves) {
-  const uint64_t most = FP8Q_LAYER_MAX_WAVES / waves < 1 ? 1 : FP8Q_LAYER_MAX_WAVES / waves;
+  const uint64_t most = max_workgroups(waves);
   const uint64_t wgs = (units + per - 1) / per;
   return (uint32_t)(wgs < 1 ? 1 : wgs < most ? wgs : most);
 }
@@ -31,6 +34,7 @@ struct NormForward {
   bool weight_bf16;
   float eps;
   uint32_t hidden;
+  float inv_hidden;           // 1 / hidden
   uint64_t rows;
   void *h_out;                // or null
   void *y_out;                // or null
@@ -50,6 +54,7 @@ struct NormBackward {
   const float *rstd;
   const void *dh;             // or null
   uint32_t hidden;
+  float inv_hidden;           // 1 / hidden
   uint64_t rows;              // 0 is allowed: dweight is cleared
   void *dx;
   float *dweight;

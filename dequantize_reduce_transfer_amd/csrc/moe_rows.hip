@@ -69,24 +69,27 @@ __global__ __launch_bounds__(64 * kWaves) void permute_kernel(MoePermute a, uint
 
 constexpr int kBf16 = 0, kE4m3 = 1, kE5m2 = 2, kMx8 = 3;   // fp8q_row_format
 
-// Eight values of an expert row, from element e on (n of them exist).
-template <int FMT>
-__device__ __forceinline__ void row_values(const MoeCombine &a, uint64_t slot, uint64_t e, int n,
-                                           float (&f)[8]) {
+// Eight values of the expert row `slot`, from column e on (zeros past its end).
+template <int FMT, Edge EDGE>
+__device__ __forceinline__ void row_values(const MoeCombine &a, uint64_t slot, uint32_t e,
+                                           uint32_t hidden, float (&f)[8]) {
   if constexpr (FMT == kBf16) {
-    widen8(load8_bf16<false>(static_cast<const uint16_t *>(a.rows) + slot * a.hidden + e, n), f);
+    const uint16_t *row = static_cast<const uint16_t *>(a.rows) + slot * hidden;
+    widen8(take8_bf16<EDGE>(load8_bf16<EDGE, false>(row, e, hidden), e, hidden), f);
   } else {
-    const u32x2 q = load8_codes<false>(static_cast<const uint8_t *>(a.rows) + slot * a.hidden + e, n);
+    const uint8_t *row = static_cast<const uint8_t *>(a.rows) + slot * hidden;
+    const u32x2 q = take8_codes<EDGE>(load8_codes<EDGE, false>(row, e, hidden), e, hidden);
+    const uint32_t c = e < hidden ? e : 0u;
     if constexpr (FMT == kMx8) {
-      const uint32_t s = static_cast<const uint8_t *>(a.scales)[slot * (a.hidden / kMxBlock) + e / kMxBlock];
+      const uint32_t s = static_cast<const uint8_t *>(a.scales)[slot * (hidden / kMxBlock) + c / kMxBlock];
       const f32x2 v0 = mx_dec2<false>(q.x, s), v1 = mx_dec2<true>(q.x, s);
       const f32x2 v2 = mx_dec2<false>(q.y, s), v3 = mx_dec2<true>(q.y, s);
       f[0] = v0[0], f[1] = v0[1], f[2] = v1[0], f[3] = v1[1];
       f[4] = v2[0], f[5] = v2[1], f[6] = v3[0], f[7] = v3[1];
     } else {
       constexpr int F = FMT == kE4m3 ? 0 : 1;
-      const uint64_t blocks = (a.hidden + kBlock - 1) / kBlock;
-      const float s = static_cast<const float *>(a.scales)[slot * blocks + e / kBlock];
+      const uint64_t blocks = (hidden + kBlock - 1) / kBlock;
+      const float s = static_cast<const float *>(a.scales)[slot * blocks + c / kBlock];
       const f32x2 v0 = dec2<F, false>(q.x), v1 = dec2<F, true>(q.x);
       const f32x2 v2 = dec2<F, false>(q.y), v3 = dec2<F, true>(q.y);
       f[0] = v0[0] * s, f[1] = v0[1] * s, f[2] = v1[0] * s, f[3] = v1[1] * s;
@@ -96,65 +99,57 @@ __device__ __forceinline__ void row_values(const MoeCombine &a, uint64_t slot, u
 }
 
 // One wave a (token, 512 columns).
-template <int FMT>
-__global__ __launch_bounds__(64 * kWaves) void combine_kernel(MoeCombine a, uint64_t pieces) {
+template <int FMT, Edge EDGE>
+__global__ __launch_bounds__(64 * kWaves) void combine_kernel(MoeCombine a, uint32_t pieces) {
   const uint64_t units = (uint64_t)a.tokens * pieces;
+  const uint32_t hidden = (uint32_t)a.hidden;
   for (uint64_t u = (uint64_t)blockIdx.x * kWaves + uniform(threadIdx.x / kWave); u < units;
        u += (uint64_t)gridDim.x * kWaves) {
-    const uint64_t t = u / pieces, e = (u % pieces) * kColumns + 8 * lane_id();
-    if (e >= a.hidden) continue;
-    const uint64_t left = a.hidden - e;
-    const int n = left < 8 ? (int)left : 8;
+    const uint64_t t = u / pieces;
+    const uint32_t e = (uint32_t)(u % pieces) * kColumns + 8 * lane_id();
     float acc[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
     for (uint32_t j = 0; j < a.topk; ++j) {
       const int slot = a.slots[t * a.topk + j];
       if (slot < 0 || (uint64_t)slot >= a.row_count) continue;
       const float w = a.weights ? a.weights[t * a.topk + j] : 1.0f;
       float f[8];
-      row_values<FMT>(a, (uint64_t)slot, e, n, f);
+      row_values<FMT, EDGE>(a, (uint64_t)slot, e, hidden, f);
 #pragma unroll
       for (int i = 0; i < 8; ++i) acc[i] = __builtin_fmaf(w, f[i], acc[i]);
     }
-    if (a.out_bf16) {
-      store8_bf16<false>(static_cast<uint16_t *>(a.out) + t * a.hidden + e, round8_bf16(acc), n);
-    } else {
-      float *o = static_cast<float *>(a.out) + t * a.hidden + e;
-      if (n == 8) {
-        *reinterpret_cast<f32x4_el4 *>(o) = f32x4{acc[0], acc[1], acc[2], acc[3]};
-        *reinterpret_cast<f32x4_el4 *>(o + 4) = f32x4{acc[4], acc[5], acc[6], acc[7]};
-      } else {
-#pragma unroll
-        for (int i = 0; i < 7; ++i)
-          if (i < n) o[i] = acc[i];
-      }
+    if (e < hidden) {
+      if (a.out_bf16)
+        store8_bf16<EDGE, false>(static_cast<uint16_t *>(a.out) + t * hidden, e, hidden, round8_bf16(acc));
+      else
+        store8_f32<EDGE, false>(static_cast<float *>(a.out) + t * hidden, e, hidden, acc);
     }
   }
 }
 
 // One wave a (token, choice): the row's products with dy, and its gradient.
+template <Edge EDGE>
 __global__ __launch_bounds__(64 * kWaves) void combine_backward_kernel(MoeCombineBackward a) {
   const uint64_t pairs = (uint64_t)a.tokens * a.topk;
+  const uint32_t hidden = (uint32_t)a.hidden;
   for (uint64_t p = (uint64_t)blockIdx.x * kWaves + uniform(threadIdx.x / kWave); p < pairs;
        p += (uint64_t)gridDim.x * kWaves) {
     const int slot = a.slots[p];
     float dot = 0.0f;
     if (slot >= 0 && (uint64_t)slot < a.row_count) {
       const float w = a.weights[p];
-      const uint16_t *dy = static_cast<const uint16_t *>(a.dy) + p / a.topk * a.hidden;
-      const uint16_t *row = static_cast<const uint16_t *>(a.rows) + (uint64_t)slot * a.hidden;
-      uint16_t *drow = static_cast<uint16_t *>(a.drows) + (uint64_t)slot * a.hidden;
-      for (uint64_t e = 8 * lane_id(); e < a.hidden; e += kColumns) {
-        const uint64_t left = a.hidden - e;
-        const int n = left < 8 ? (int)left : 8;
+      const uint16_t *dy = static_cast<const uint16_t *>(a.dy) + p / a.topk * hidden;
+      const uint16_t *row = static_cast<const uint16_t *>(a.rows) + (uint64_t)slot * hidden;
+      uint16_t *drow = static_cast<uint16_t *>(a.drows) + (uint64_t)slot * hidden;
+      for (uint32_t e = 8 * lane_id(); e < hidden; e += kColumns) {
         float g[8], r[8], d[8];
-        widen8(load8_bf16<false>(dy + e, n), g);
-        widen8(load8_bf16<false>(row + e, n), r);
+        widen8(take8_bf16<EDGE>(load8_bf16<EDGE, false>(dy, e, hidden), e, hidden), g);
+        widen8(take8_bf16<EDGE>(load8_bf16<EDGE, false>(row, e, hidden), e, hidden), r);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          if (i < n) dot = __builtin_fmaf(g[i], r[i], dot);
+          dot = __builtin_fmaf(g[i], r[i], dot);
           d[i] = w * g[i];
         }
-        store8_bf16<false>(drow + e, round8_bf16(d), n);
+        store8_bf16<EDGE, false>(drow, e, hidden, round8_bf16(d));
       }
       dot = sum_wave(dot);
     }
@@ -172,22 +167,34 @@ hipError_t launch_moe_permute(const MoePermute &a, hipStream_t stream) {
   return hipGetLastError();
 }
 
-hipError_t launch_moe_combine(int format, const MoeCombine &a, hipStream_t stream) {
-  const uint64_t pieces = (a.hidden + kColumns - 1) / kColumns;
+template <int FMT>
+static void combine_launch(const MoeCombine &a, hipStream_t stream) {
+  const uint32_t pieces = (uint32_t)((a.hidden + kColumns - 1) / kColumns);
   const dim3 grid(grid_for((uint64_t)a.tokens * pieces, kWaves, kWaves)), block(64 * kWaves);
+  switch (edge_of(a.hidden)) {
+    case kEven: hipLaunchKernelGGL((combine_kernel<FMT, kEven>), grid, block, 0, stream, a, pieces); break;
+    case kOdd: hipLaunchKernelGGL((combine_kernel<FMT, kOdd>), grid, block, 0, stream, a, pieces); break;
+    default: hipLaunchKernelGGL((combine_kernel<FMT, kTiny>), grid, block, 0, stream, a, pieces); break;
+  }
+}
+
+hipError_t launch_moe_combine(int format, const MoeCombine &a, hipStream_t stream) {
   switch (format) {
-    case kBf16: hipLaunchKernelGGL((combine_kernel<kBf16>), grid, block, 0, stream, a, pieces); break;
-    case kE4m3: hipLaunchKernelGGL((combine_kernel<kE4m3>), grid, block, 0, stream, a, pieces); break;
-    case kE5m2: hipLaunchKernelGGL((combine_kernel<kE5m2>), grid, block, 0, stream, a, pieces); break;
-    default: hipLaunchKernelGGL((combine_kernel<kMx8>), grid, block, 0, stream, a, pieces); break;
+    case kBf16: combine_launch<kBf16>(a, stream); break;
+    case kE4m3: combine_launch<kE4m3>(a, stream); break;
+    case kE5m2: combine_launch<kE5m2>(a, stream); break;
+    default: combine_launch<kMx8>(a, stream); break;
   }
   return hipGetLastError();
 }
 
 hipError_t launch_moe_combine_backward(const MoeCombineBackward &a, hipStream_t stream) {
-  hipLaunchKernelGGL(combine_backward_kernel,
-                     dim3(grid_for((uint64_t)a.tokens * a.topk, kWaves, kWaves)),
-                     dim3(64 * kWaves), 0, stream, a);
+  const dim3 grid(grid_for((uint64_t)a.tokens * a.topk, kWaves, kWaves)), block(64 * kWaves);
+  switch (edge_of(a.hidden)) {
+    case kEven: hipLaunchKernelGGL((combine_backward_kernel<kEven>), grid, block, 0, stream, a); break;
+    case kOdd: hipLaunchKernelGGL((combine_backward_kernel<kOdd>), grid, block, 0, stream, a); break;
+    default: hipLaunchKernelGGL((combine_backward_kernel<kTiny>), grid, block, 0, stream, a); break;
+  }
   return hipGetLastError();
 }
 

@@ -13,11 +13,26 @@
 // A lane holds eight consecutive elements of a vector (16-byte loads), so a
 // block of 128 is a 16-lane row and a block of 32 a quad: the block maxima
 // are DPP steps, and no LDS is used but for the sum over the row's waves.
+// Waves are added before vectors: a row of up to 4096 is spread so that each
+// lane has one vector, which measured best on MI355X (65536 rows of 2048,
+// e4m3, residual: 146 us with 4 waves x 1 vector, 152 with 2 x 2, 154 with
+// 1 x 4).  What is left above HBM's own time is instructions, so the kernel has
+// no row loop (the host splits launches beyond the grid limit): bases stay in
+// scalar registers and lane offsets in 32 bits.  Non-temporal loads and
+// stores, and runs of 64 workgroups an XCD, are worth 2-5% at large sizes.
+// Measured (median, rotating inputs): 16384 x 8192 e4m3 with residual 151 us,
+// 6.24 TB/s, where a plain stream with the same 4 bytes in and 3 out reaches
+// 6.36; 65536 x 2048 146 us, 6.45 TB/s; one row of 2048 2.0 us in a graph.
 //
 // Backward: dx needs one sum over the row, dweight one over the rows.  A
-// workgroup walks rows, keeps its dweight sums in registers, and writes them
-// once into the workspace; a second kernel adds the workgroups' parts in a
-// fixed order.
+// workgroup walks rows, each row's loads issued a row ahead, keeps its
+// dweight sums in registers, and writes them once into the workspace; a
+// second kernel adds the workgroups' parts in a fixed order.  Fewer
+// workgroups mean fewer parts to write and read back, more of them more loads
+// in flight: 2048 waves measured best (16384 x 4096 with the residual's
+// gradient, 8 bytes an element: 87 us, 6.2 TB/s, with 256 workgroups of 8
+// waves; 89 with 512, 92 with 1024; 32768 x 2048 in 4-wave workgroups: 88 us
+// with 512, 112 with 256, 92 with 1024).
 #include "f32_encode.h"
 #include "fp8q_device.h"
 #include "layer_device.h"
@@ -26,6 +41,19 @@
 namespace fp8q {
 namespace {
 
+#ifndef NLD
+#define NLD true
+#endif
+#ifndef NST
+#define NST true
+#endif
+#ifndef XC
+#define XC 64
+#endif
+#ifndef NW
+#define NW 8
+#define NV 2
+#endif
 constexpr int kMx8 = 2;          // OUT: 0 = E4M3, 1 = E5M2 (fp32 scales), 2 = MXFP8
 
 // Sum over the W waves that share a row; every thread gets it.  `part` is W
@@ -34,7 +62,7 @@ template <int W>
 __device__ __forceinline__ float sum_row(float v, float *part) {
   v = sum_wave(v);
   if constexpr (W > 1) {
-    const uint32_t wid = uniform(threadIdx.x / kWave);
+    const uint32_t wid = uniform(threadIdx.x / kWave) % W;
     if (lane_id() == 0) part[wid] = v;
     __syncthreads();
     v = part[0];
@@ -66,9 +94,7 @@ __device__ __forceinline__ MxF32 mx_f32_scale(uint32_t amax_bits) {
 // scale's bits, or an E8M0 code.
 template <int OUT>
 __device__ __forceinline__ u32x2 encode8(const float (&y)[8], uint32_t *scale) {
-  uint32_t m = abs_bits(y[0]);
-#pragma unroll
-  for (int j = 1; j < 8; ++j) m = m > abs_bits(y[j]) ? m : abs_bits(y[j]);
+  const uint32_t m = amax8_bits(y);
   u32x2 q;
   bool finite;
   if constexpr (OUT == kMx8) {
@@ -83,225 +109,320 @@ __device__ __forceinline__ u32x2 encode8(const float (&y)[8], uint32_t *scale) {
     const F32Scale s = f32_block_scale<OUT>(max_row16(m));
     *scale = __float_as_uint(s.s);
     finite = s.finite;
-    q = quot8<OUT, true>(y, s);
+    if (wave_any(s.f != 1.0f))
+      q = quot8<OUT, true>(y, s);
+    else
+      q = quot8<OUT, false>(y, s);
   }
   if (!finite) q = u32x2{0x7F7F7F7Fu, 0x7F7F7F7Fu};
   return q;
 }
 
 // One row per W waves, V vectors of eight elements a lane (W * V * 512 >=
-// hidden); workgroups of max(W, 4) waves.  The grid covers the rows, and
-// beyond the grid limit the workgroups stride; the row sum's LDS slot
-// alternates between rounds, so the one barrier inside it is enough.
-template <int OUT, bool RES, int W, int V>
+// hidden); workgroups of max(W, 4) waves.
+template <int OUT, bool RES, bool WB, Edge EDGE, int W, int V>
 __global__ __launch_bounds__(64 * (W > 4 ? W : 4)) void norm_kernel(NormForward a) {
   constexpr int kRows = W >= 4 ? 1 : 4 / W;              // rows a workgroup
   constexpr uint32_t kThreads = 64 * W;                  // threads a row
-  __shared__ float part[2][kRows * W];
+  __shared__ float part[kRows * W];
   const uint32_t sub = W >= 4 ? 0 : uniform(threadIdx.x / kThreads);
   const uint32_t tid = threadIdx.x % kThreads;
-  const int hidden = (int)a.hidden;
-  uint32_t turn = 0;
-  for (uint64_t row0 = (uint64_t)blockIdx.x * kRows; row0 < a.rows;
-       row0 += (uint64_t)gridDim.x * kRows, turn ^= 1) {
-    const uint64_t row = row0 + sub;
-    const bool live = row < a.rows;                      // uniform over the row's waves
-    const uint64_t base = (live ? row : 0) * (uint64_t)a.hidden;
-    const uint16_t *x = static_cast<const uint16_t *>(a.x) + base;
-    const uint16_t *r = RES ? static_cast<const uint16_t *>(a.residual) + base : nullptr;
+  const uint32_t hidden = a.hidden;
+  const uint64_t row0 = (uint64_t)block_position() * kRows;
+  const bool live = row0 + sub < a.rows;                 // the same for the row's waves
+  const uint64_t row = live ? row0 + sub : row0;
+  const uint64_t base = row * (uint64_t)hidden;
+  const uint16_t *x = static_cast<const uint16_t *>(a.x) + base;
+  const uint16_t *r = static_cast<const uint16_t *>(a.residual) + base;
 
-    u32x4 xv[V], rv[V];
+  u32x4 xv[V], rv[V];
+  Weights8<EDGE, WB> wv[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int e = 8 * (int)(v * kThreads + tid), n = hidden - e;
-      xv[v] = rv[v] = u32x4{0u, 0u, 0u, 0u};
-      if (live && n > 0) {
-        xv[v] = load8_bf16<false>(x + e, n);
-        if constexpr (RES) rv[v] = load8_bf16<false>(r + e, n);
-      }
+  for (int v = 0; v < V; ++v) {
+    const uint32_t e = 8 * (v * kThreads + tid);
+    xv[v] = load8_bf16<EDGE, true>(x, e, hidden);
+    if constexpr (RES) rv[v] = load8_bf16<EDGE, true>(r, e, hidden);
+  }
+#pragma unroll
+  for (int v = 0; v < V; ++v) wv[v].load(a.weight, 8 * (v * kThreads + tid), hidden);
+  loads_issued();
+  float h[V][8];
+  float ss = 0.0f;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const uint32_t e = 8 * (v * kThreads + tid);
+    widen8(take8_bf16<EDGE>(xv[v], e, hidden), h[v]);
+    if constexpr (RES) {
+      float t[8];
+      widen8(take8_bf16<EDGE>(rv[v], e, hidden), t);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) h[v][j] += t[j];
     }
-    float h[V][8];
-    float ss = 0.0f;
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      widen8(xv[v], h[v]);
-      if constexpr (RES) {
-        float t[8];
-        widen8(rv[v], t);
+    for (int j = 0; j < 8; ++j) ss = __builtin_fmaf(h[v][j], h[v][j], ss);
+  }
+  ss = sum_row<W>(ss, part + sub * W);
+  if (!live) return;
+  const float rstd = rsqrtf(__builtin_fmaf(ss, a.inv_hidden, a.eps));
+  if (a.rstd_out && tid == 0) a.rstd_out[row] = rstd;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) h[v][j] += t[j];
-      }
+  for (int v = 0; v < V; ++v) {
+    const uint32_t i = v * kThreads + tid, e = 8 * i;    // the lane's vector of the row
+    float y[8], w[8];
+    wv[v].take(e, hidden, w);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) ss = __builtin_fmaf(h[v][j], h[v][j], ss);
+    for (int j = 0; j < 8; ++j) y[j] = (h[v][j] * rstd) * w[j];
+    if (EDGE == kEven ? e >= hidden : e + 8u > hidden) {           // 0 * inf where rstd is not finite
+#pragma unroll
+      for (uint32_t j = 0; j < 8; ++j) y[j] = e + j < hidden ? y[j] : 0.0f;
     }
-    ss = sum_row<W>(ss, part[turn] + sub * W);
-    const float rstd = 1.0f / sqrtf(ss / (float)hidden + a.eps);
-    if (!live) continue;
-    if (a.rstd_out && tid == 0) a.rstd_out[row] = rstd;
-
-    uint16_t *ho = a.h_out ? static_cast<uint16_t *>(a.h_out) + base : nullptr;
-    uint16_t *yo = a.y_out ? static_cast<uint16_t *>(a.y_out) + base : nullptr;
-    uint8_t *q = static_cast<uint8_t *>(a.q_out) + base;
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const uint32_t i = v * kThreads + tid;             // the lane's vector of the row
-      const int e = 8 * (int)i, n = hidden - e;
-      float y[8];
-      if (n > 0) {
-        float w[8];
-        load8_weight(a.weight, a.weight_bf16, e, n, w);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) y[j] = j < n ? (h[v][j] * rstd) * w[j] : 0.0f;
+    uint32_t scale;
+    const u32x2 codes = encode8<OUT>(y, &scale);
+    if (e < hidden) {
+      if (RES && a.h_out)
+        store8_bf16<EDGE, true>(static_cast<uint16_t *>(a.h_out) + base, e, hidden, round8_bf16(h[v]));
+      if (a.y_out)
+        store8_bf16<EDGE, true>(static_cast<uint16_t *>(a.y_out) + base, e, hidden, round8_bf16(y));
+      store8_codes<EDGE, true>(static_cast<uint8_t *>(a.q_out) + base, e, hidden, codes);
+      if constexpr (OUT == kMx8) {
+        uint8_t *scales = static_cast<uint8_t *>(a.scales_out) + row * (hidden / kMxBlock);
+        if ((i & 3) == 0) scales[i / 4] = (uint8_t)scale;
       } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) y[j] = 0.0f;
-      }
-      uint32_t scale;
-      const u32x2 codes = encode8<OUT>(y, &scale);
-      if (n > 0) {
-        if (RES && ho) store8_bf16<false>(ho + e, round8_bf16(h[v]), n);
-        if (yo) store8_bf16<false>(yo + e, round8_bf16(y), n);
-        store8_codes<false>(q + e, codes, n);
-        if constexpr (OUT == kMx8) {
-          if ((i & 3) == 0)
-            static_cast<uint8_t *>(a.scales_out)[row * (a.hidden / kMxBlock) + i / 4] = (uint8_t)scale;
-        } else {
-          const uint32_t blocks = (a.hidden + kBlock - 1) / kBlock;
-          if ((i & 15) == 0)
-            static_cast<uint32_t *>(a.scales_out)[row * (uint64_t)blocks + i / 16] = scale;
-        }
+        uint32_t *scales = static_cast<uint32_t *>(a.scales_out) + row * ((hidden + kBlock - 1) / kBlock);
+        if ((i & 15) == 0) scales[i / 16] = scale;
       }
     }
   }
 }
 
-template <int OUT, bool RES, int W, int V>
-hipError_t norm_launch(const NormForward &a, hipStream_t stream) {
+// Launches over all rows, in grids of at most kMaxGrid workgroups.
+template <int OUT, bool RES, bool WB, Edge EDGE, int W, int V>
+hipError_t norm_launch(NormForward a, hipStream_t stream) {
   constexpr int kRows = W >= 4 ? 1 : 4 / W, kWgWaves = W > 4 ? W : 4;
-  hipLaunchKernelGGL((norm_kernel<OUT, RES, W, V>), dim3(grid_for(a.rows, kRows, kWgWaves)),
-                     dim3(64 * kWgWaves), 0, stream, a);
+  constexpr uint64_t kMost = max_workgroups(kWgWaves) * kRows;
+  const uint64_t blocks = OUT == kMx8 ? a.hidden / kMxBlock : (a.hidden + kBlock - 1) / kBlock;
+  for (uint64_t left = a.rows; left;) {
+    const uint64_t rows = left < kMost ? left : kMost, n = rows * a.hidden;
+    a.rows = rows;
+    hipLaunchKernelGGL((norm_kernel<OUT, RES, WB, EDGE, W, V>), dim3((uint32_t)((rows + kRows - 1) / kRows)),
+                       dim3(64 * kWgWaves), 0, stream, a);
+    left -= rows;
+    if (!left) break;
+    a.x = static_cast<const uint16_t *>(a.x) + n;
+    if (RES) a.residual = static_cast<const uint16_t *>(a.residual) + n;
+    if (a.h_out) a.h_out = static_cast<uint16_t *>(a.h_out) + n;
+    if (a.y_out) a.y_out = static_cast<uint16_t *>(a.y_out) + n;
+    a.q_out = static_cast<uint8_t *>(a.q_out) + n;
+    a.scales_out = static_cast<uint8_t *>(a.scales_out) + rows * blocks * (OUT == kMx8 ? 1 : 4);
+    if (a.rstd_out) a.rstd_out += rows;
+  }
   return hipGetLastError();
 }
 
-template <int OUT, bool RES>
+template <int OUT, bool RES, bool WB, Edge EDGE>
 hipError_t norm_dispatch(const NormForward &a, hipStream_t stream) {
-  if (a.hidden <= 2048) return norm_launch<OUT, RES, 4, 1>(a, stream);
-  if (a.hidden <= 4096) return norm_launch<OUT, RES, 4, 2>(a, stream);
-  if (a.hidden <= 8192) return norm_launch<OUT, RES, 4, 4>(a, stream);
-  if (a.hidden <= 16384) return norm_launch<OUT, RES, 8, 4>(a, stream);
-  return norm_launch<OUT, RES, 16, 4>(a, stream);
+  if constexpr (EDGE == kTiny) return norm_launch<OUT, RES, WB, kTiny, 1, 1>(a, stream);
+  if (a.hidden <= 512) return norm_launch<OUT, RES, WB, EDGE, 1, 1>(a, stream);
+  if (a.hidden <= 1024) return norm_launch<OUT, RES, WB, EDGE, 2, 1>(a, stream);
+  if (a.hidden <= 2048) return norm_launch<OUT, RES, WB, EDGE, 4, 1>(a, stream);
+  if (a.hidden <= 4096) return norm_launch<OUT, RES, WB, EDGE, 8, 1>(a, stream);
+  if (a.hidden <= 8192) return norm_launch<OUT, RES, WB, EDGE, 8, 2>(a, stream);
+  if (a.hidden <= 16384) return norm_launch<OUT, RES, WB, EDGE, 16, 2>(a, stream);
+  return norm_launch<OUT, RES, WB, EDGE, 16, 4>(a, stream);
 }
 
-// A workgroup of W waves walks rows blockIdx.x, blockIdx.x + gridDim.x, ...;
-// its dweight sums go to parts[blockIdx.x] (or, alone, to dweight itself).
-// The row sum's LDS slot alternates, so one barrier a row is enough: a wave
-// that is a row ahead writes the other slot, and it can only be two ahead
-// once every wave has passed the barrier between.
-template <int W, int V>
-__global__ __launch_bounds__(64 * W) void norm_backward_kernel(NormBackward a, float *parts) {
-  constexpr uint32_t kThreads = 64 * W;
-  __shared__ float part[2][W];
-  const uint32_t tid = threadIdx.x;
-  const int hidden = (int)a.hidden;
+template <int OUT, Edge EDGE>
+hipError_t norm_rows(const NormForward &a, hipStream_t stream) {
+  if (a.residual)
+    return a.weight_bf16 ? norm_dispatch<OUT, true, true, EDGE>(a, stream)
+                         : norm_dispatch<OUT, true, false, EDGE>(a, stream);
+  return a.weight_bf16 ? norm_dispatch<OUT, false, true, EDGE>(a, stream)
+                       : norm_dispatch<OUT, false, false, EDGE>(a, stream);
+}
+
+// Floats from one workgroup's dweight sums to the next one's in the workspace.
+__host__ __device__ constexpr uint32_t part_stride(uint32_t hidden) { return (hidden + 7) / 8 * 8; }
+
+// What a lane holds of a row.
+template <Edge EDGE, int W, int V>
+struct BackwardRow {
+  u32x4 dy[V], h[V], dh[V];
+  float rstd;
+  __device__ __forceinline__ void load(const NormBackward &a, uint64_t row, uint32_t tid) {
+    uint64_t base = row * (uint64_t)a.hidden;
+    asm volatile("" : "+s"(base));       // keeps a scalar base and 32-bit offsets in the row loop
+    const uint16_t *yp = static_cast<const uint16_t *>(a.dy) + base;
+    const uint16_t *hp = static_cast<const uint16_t *>(a.h) + base;
+    const uint16_t *sp = static_cast<const uint16_t *>(a.dh) + base;
+    rstd = a.rstd[row];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const uint32_t e = 8 * (v * 64 * W + tid);
+      dy[v] = load8_bf16<EDGE, true>(yp, e, a.hidden);
+      h[v] = load8_bf16<EDGE, true>(hp, e, a.hidden);
+      if (a.dh) dh[v] = load8_bf16<EDGE, true>(sp, e, a.hidden);
+    }
+    loads_issued();
+  }
+};
+
+// W waves walk rows, each row's loads issued before the sum of the one
+// before; workgroups of max(W, 4) waves.  A workgroup's dweight sums go to
+// parts[blockIdx.x] (or, alone, to dweight itself).  The row sum's LDS slot
+// alternates, so one barrier a row is enough: a wave that is a row ahead
+// writes the other slot, and it can only be two ahead once every wave has
+// passed the barrier between.
+template <bool WB, Edge EDGE, int W, int V>
+__global__ __launch_bounds__(64 * (W > 4 ? W : 4)) void norm_backward_kernel(NormBackward a, float *parts) {
+  constexpr int kRows = W >= 4 ? 1 : 4 / W;              // rows a workgroup has in hand
+  constexpr uint32_t kThreads = 64 * W;                  // threads a row
+  __shared__ float part[2][kRows * W];
+  __shared__ float joined[kRows > 1 ? (kRows - 1) * kThreads * V * 8 : 1];
+  const uint32_t sub = W >= 4 ? 0 : uniform(threadIdx.x / kThreads);
+  const uint32_t tid = threadIdx.x % kThreads, hidden = a.hidden;
+  const uint64_t stride = (uint64_t)gridDim.x * kRows;
+  uint64_t row0 = (uint64_t)blockIdx.x * kRows;
+  BackwardRow<EDGE, W, V> next;
+  next.load(a, row0 + sub < a.rows ? row0 + sub : row0, tid);
   float w[V][8], dw[V][8];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    const int e = 8 * (int)(v * kThreads + tid), n = hidden - e;
+    const uint32_t e = 8 * (v * kThreads + tid);
+    Weights8<EDGE, WB> raw;
+    raw.load(a.weight, e, hidden);
+    raw.take(e, hidden, w[v]);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) w[v][j] = dw[v][j] = 0.0f;
-    if (n > 0) load8_weight(a.weight, a.weight_bf16, e, n, w[v]);
+    for (int j = 0; j < 8; ++j) dw[v][j] = 0.0f;
   }
-  uint32_t turn = 0;
-  for (uint64_t row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
-    const uint64_t base = row * (uint64_t)a.hidden;
-    const uint16_t *dy = static_cast<const uint16_t *>(a.dy) + base;
-    const uint16_t *hp = static_cast<const uint16_t *>(a.h) + base;
-    const uint16_t *dh = a.dh ? static_cast<const uint16_t *>(a.dh) + base : nullptr;
-    uint16_t *dx = static_cast<uint16_t *>(a.dx) + base;
-    const float rstd = a.rstd[row];
-    u32x4 yv[V], hv[V], sv[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int e = 8 * (int)(v * kThreads + tid), n = hidden - e;
-      yv[v] = hv[v] = sv[v] = u32x4{0u, 0u, 0u, 0u};
-      if (n > 0) {
-        yv[v] = load8_bf16<false>(dy + e, n);
-        hv[v] = load8_bf16<false>(hp + e, n);
-        if (dh) sv[v] = load8_bf16<false>(dh + e, n);
-      }
-    }
+  for (uint32_t turn = 0; row0 < a.rows; row0 += stride, turn ^= 1) {
+    const bool live = row0 + sub < a.rows;               // the same for the row's waves
+    BackwardRow<EDGE, W, V> cur = next;
+    if (row0 + stride < a.rows)
+      next.load(a, row0 + stride + sub < a.rows ? row0 + stride + sub : row0 + stride, tid);
     float sum = 0.0f;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
+      const uint32_t e = 8 * (v * kThreads + tid);
       float y[8], h[8];
-      widen8(yv[v], y);
-      widen8(hv[v], h);
+      cur.dy[v] = take8_bf16<EDGE>(cur.dy[v], e, hidden);
+      cur.h[v] = take8_bf16<EDGE>(cur.h[v], e, hidden);
+      widen8(cur.dy[v], y);
+      widen8(cur.h[v], h);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        sum = __builtin_fmaf(y[j] * w[v][j], h[j], sum);
-        dw[v][j] = __builtin_fmaf(y[j], h[j] * rstd, dw[v][j]);
+      for (int j = 0; j < 8; ++j) sum = __builtin_fmaf(y[j] * w[v][j], h[j], sum);
+      if (live) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) dw[v][j] = __builtin_fmaf(y[j], h[j] * cur.rstd, dw[v][j]);
       }
     }
-    sum = sum_row<W>(sum, part[turn]);
-    const float c = sum / (float)hidden * rstd * rstd * rstd;
+    sum = sum_row<W>(sum, part[turn] + sub * W);
+    const float c = sum * a.inv_hidden * cur.rstd * cur.rstd * cur.rstd;
+    uint64_t base = (row0 + sub) * (uint64_t)hidden;
+    asm volatile("" : "+s"(base));
+    uint16_t *dx = static_cast<uint16_t *>(a.dx) + base;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const int e = 8 * (int)(v * kThreads + tid), n = hidden - e;
-      if (n <= 0) continue;
-      float y[8], h[8], s[8], d[8];
-      widen8(yv[v], y);
-      widen8(hv[v], h);
-      widen8(sv[v], s);
+      const uint32_t e = 8 * (v * kThreads + tid);
+      float y[8], h[8], d[8];
+      widen8(cur.dy[v], y);
+      widen8(cur.h[v], h);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) d[j] = 0.0f;
+      if (a.dh) widen8(take8_bf16<EDGE>(cur.dh[v], e, hidden), d);
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        d[j] = __builtin_fmaf(-h[j], c, __builtin_fmaf(y[j] * w[v][j], rstd, s[j]));
-      store8_bf16<false>(dx + e, round8_bf16(d), n);
+        d[j] = __builtin_fmaf(-h[j], c, __builtin_fmaf(y[j] * w[v][j], cur.rstd, d[j]));
+      if (live && e < hidden) store8_bf16<EDGE, false>(dx, e, hidden, round8_bf16(d));
     }
   }
-  float *out = parts ? parts + (uint64_t)blockIdx.x * a.hidden : a.dweight;
+  if constexpr (kRows > 1) {
+    if (sub) {
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) joined[(((sub - 1) * V + v) * 8 + j) * kThreads + tid] = dw[v][j];
+    }
+    __syncthreads();
+    if (sub) return;
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+#pragma unroll
+        for (int q = 0; q < kRows - 1; ++q) dw[v][j] += joined[((q * V + v) * 8 + j) * kThreads + tid];
+  }
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    const int e = 8 * (int)(v * kThreads + tid), n = hidden - e;
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (j < n) out[e + j] = dw[v][j];
+    const uint32_t e = 8 * (v * kThreads + tid);
+    if (e >= hidden) continue;
+    if (parts)                                           // whole vectors, zeros past the row's end
+      store8_f32<kEven, false>(parts + (uint64_t)blockIdx.x * part_stride(hidden), e, hidden, dw[v]);
+    else
+      store8_f32<EDGE, false>(a.dweight, e, hidden, dw[v]);
   }
 }
 
-// dweight[e] = parts[0][e] + parts[1][e] + ...: 64 columns a workgroup, each
-// wave a run of parts, the waves' sums added in order.
+// dweight[e] = parts[0][e] + parts[1][e] + ...  A workgroup takes 64 columns,
+// a lane four of them of every 64th part (16 waves x 4 lane groups), and the
+// groups' sums are added in order.
 constexpr int kPartWaves = 16;
-__global__ __launch_bounds__(64 * kPartWaves) void norm_parts_kernel(const float *parts,
-                                                                     uint32_t count, uint32_t hidden,
-                                                                     float *dweight) {
-  __shared__ float sums[kPartWaves][64];
-  const uint32_t lane = lane_id(), wid = uniform(threadIdx.x / kWave);
-  const uint32_t e = blockIdx.x * 64 + lane;
-  const uint32_t run = (count + kPartWaves - 1) / kPartWaves;
-  const uint32_t first = wid * run, last = first + run < count ? first + run : count;
-  float s = 0.0f;
-  if (e < hidden)
-    for (uint32_t p = first; p < last; ++p) s += parts[(uint64_t)p * hidden + e];
-  sums[wid][lane] = s;
-  __syncthreads();
-  if (wid == 0 && e < hidden) {
-    s = sums[0][lane];
+constexpr int kPartGroups = 4 * kPartWaves;
+__global__ __launch_bounds__(64 * kPartWaves) void norm_parts_kernel(const float *parts, uint32_t count,
+                                                                     uint32_t hidden, float *dweight) {
+  __shared__ float sums[kPartGroups][64];
+  const uint32_t tid = threadIdx.x, group = tid / 16, c = 4 * (tid % 16);
+  const uint32_t e = blockIdx.x * 64 + c;
+  float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (e < hidden) {
+#pragma unroll 8
+    for (uint32_t p = group; p < count; p += kPartGroups) {
+      const f32x4 v = __builtin_bit_cast(f32x4, load16<false>(parts + (uint64_t)p * part_stride(hidden) + e));
 #pragma unroll
-    for (int w = 1; w < kPartWaves; ++w) s += sums[w][lane];
-    dweight[e] = s;
+      for (int j = 0; j < 4; ++j) s[j] += v[j];
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) sums[group][c + j] = s[j];
+  __syncthreads();
+  const uint32_t column = blockIdx.x * 64 + tid;
+  if (tid < 64 && column < hidden) {
+    float t = sums[0][tid];
+#pragma unroll
+    for (int g = 1; g < kPartGroups; ++g) t += sums[g][tid];
+    dweight[column] = t;
   }
 }
 
-// Workgroups of the backward kernel: at most kBackwardWgs.
-constexpr uint64_t kBackwardWgs = 1024;
-uint32_t backward_wgs(uint64_t rows) { return (uint32_t)(rows < kBackwardWgs ? rows : kBackwardWgs); }
+// The backward kernel's shape by hidden: W waves a row and V vectors a lane
+// (one vector up to 4096, so that the sums of two waves more cost no more
+// registers), and its workgroups, at most: 2048 waves in all, and one
+// workgroup a CU at least.
+struct BackwardShape {
+  uint32_t rows;               // rows a workgroup has in hand
+  uint32_t most;               // workgroups
+};
+constexpr BackwardShape backward_shape(uint32_t hidden) {
+  if (hidden <= 512) return {4, 512};
+  if (hidden <= 1024) return {2, 512};
+  return {1, hidden <= 2048 ? 512u : 256u};
+}
 
-template <int W, int V>
+// Up to kOneWorkgroupRows rows one workgroup walks them all and writes dweight
+// itself: no workspace and no second launch.
+constexpr uint64_t kOneWorkgroupRows = 4;
+uint32_t backward_wgs(uint64_t rows, uint32_t hidden) {
+  if (rows <= kOneWorkgroupRows) return rows ? 1 : 0;
+  const BackwardShape shape = backward_shape(hidden);
+  const uint64_t wgs = (rows + shape.rows - 1) / shape.rows;
+  return (uint32_t)(wgs < shape.most ? wgs : shape.most);
+}
+
+template <bool WB, Edge EDGE, int W, int V>
 hipError_t backward_launch(const NormBackward &a, hipStream_t stream) {
-  const uint32_t wgs = backward_wgs(a.rows);
+  const uint32_t wgs = backward_wgs(a.rows, a.hidden);
   float *parts = wgs > 1 ? a.workspace : nullptr;
   if (wgs) {
-    hipLaunchKernelGGL((norm_backward_kernel<W, V>), dim3(wgs), dim3(64 * W), 0, stream, a, parts);
+    hipLaunchKernelGGL((norm_backward_kernel<WB, EDGE, W, V>), dim3(wgs), dim3(64 * (W > 4 ? W : 4)), 0, stream, a, parts);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
@@ -313,24 +434,48 @@ hipError_t backward_launch(const NormBackward &a, hipStream_t stream) {
 
 }  // namespace
 
+template <int OUT>
+static hipError_t norm_edges(const NormForward &a, hipStream_t stream) {
+  switch (edge_of(a.hidden)) {
+    case kEven: return norm_rows<OUT, kEven>(a, stream);
+    case kOdd: return norm_rows<OUT, kOdd>(a, stream);
+    default: return norm_rows<OUT, kTiny>(a, stream);
+  }
+}
+
 hipError_t launch_rms_norm(int out, const NormForward &a, hipStream_t stream) {
-  const bool res = a.residual != nullptr;
-  if (out == 0) return res ? norm_dispatch<0, true>(a, stream) : norm_dispatch<0, false>(a, stream);
-  if (out == 1) return res ? norm_dispatch<1, true>(a, stream) : norm_dispatch<1, false>(a, stream);
-  return res ? norm_dispatch<kMx8, true>(a, stream) : norm_dispatch<kMx8, false>(a, stream);
+  if (out == kMx8) return norm_rows<kMx8, kEven>(a, stream);   // hidden % 32 == 0
+  return out == 0 ? norm_edges<0>(a, stream) : norm_edges<1>(a, stream);
 }
 
 uint64_t norm_backward_workspace(uint64_t rows, uint32_t hidden) {
-  const uint32_t wgs = backward_wgs(rows);
-  return wgs > 1 ? 4ull * wgs * hidden : 0;
+  const uint32_t wgs = backward_wgs(rows, hidden);
+  return wgs > 1 ? 4ull * wgs * part_stride(hidden) : 0;
+}
+
+template <bool WB, Edge EDGE>
+static hipError_t backward_dispatch(const NormBackward &a, hipStream_t stream) {
+  if constexpr (EDGE == kTiny) return backward_launch<WB, kTiny, 1, 1>(a, stream);
+  if (a.hidden <= 512) return backward_launch<WB, EDGE, 1, 1>(a, stream);
+  if (a.hidden <= 1024) return backward_launch<WB, EDGE, 2, 1>(a, stream);
+  if (a.hidden <= 2048) return backward_launch<WB, EDGE, 4, 1>(a, stream);
+  if (a.hidden <= 4096) return backward_launch<WB, EDGE, 8, 1>(a, stream);
+  if (a.hidden <= 8192) return backward_launch<WB, EDGE, 8, 2>(a, stream);
+  if (a.hidden <= 16384) return backward_launch<WB, EDGE, 16, 2>(a, stream);
+  return backward_launch<WB, EDGE, 16, 4>(a, stream);
+}
+
+template <bool WB>
+static hipError_t backward_edges(const NormBackward &a, hipStream_t stream) {
+  switch (edge_of(a.hidden)) {
+    case kEven: return backward_dispatch<WB, kEven>(a, stream);
+    case kOdd: return backward_dispatch<WB, kOdd>(a, stream);
+    default: return backward_dispatch<WB, kTiny>(a, stream);
+  }
 }
 
 hipError_t launch_rms_norm_backward(const NormBackward &a, hipStream_t stream) {
-  if (a.hidden <= 2048) return backward_launch<4, 1>(a, stream);
-  if (a.hidden <= 4096) return backward_launch<4, 2>(a, stream);
-  if (a.hidden <= 8192) return backward_launch<8, 2>(a, stream);
-  if (a.hidden <= 16384) return backward_launch<16, 2>(a, stream);
-  return backward_launch<16, 4>(a, stream);
+  return a.weight_bf16 ? backward_edges<true>(a, stream) : backward_edges<false>(a, stream);
 }
 
 }  // namespace fp8q
