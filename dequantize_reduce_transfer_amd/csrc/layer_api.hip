@@ -181,7 +181,8 @@ fp8q_status fp8q_moe_permute(const void *src, size_t row_bytes, const void *src_
   if (row_bytes == 0 && scale_row_bytes != 0) return FP8Q_ERR_ARG;
   if (tokens == 0 || dst_rows == 0 || row_bytes == 0) return FP8Q_OK;
   for (const size_t bytes : {row_bytes, scale_row_bytes})
-    if (bytes && (!size_ok(tokens, bytes) || !size_ok(dst_rows, bytes))) return FP8Q_ERR_ARG;
+    if (bytes > 4 * FP8Q_MAX_HIDDEN || (bytes && (!size_ok(tokens, bytes) || !size_ok(dst_rows, bytes))))
+      return FP8Q_ERR_ARG;
   if (!src || !slots || !dst) return FP8Q_ERR_NULL;
   if (scale_row_bytes && (!src_scales || !dst_scales)) return FP8Q_ERR_NULL;
   if (!aligned(src, 16) || !aligned(dst, 16) || !aligned(slots, 4)) return FP8Q_ERR_ALIGN;
@@ -206,7 +207,7 @@ fp8q_status fp8q_moe_combine(const void *rows, fp8q_row_format format, const voi
   if (!pairs_ok(tokens, topk) || row_count > FP8Q_MAX_PAIRS) return FP8Q_ERR_ARG;
   if (format == FP8Q_ROWS_MX8 && hidden % FP8Q_MX_BLOCK != 0) return FP8Q_ERR_ARG;
   if (tokens == 0 || hidden == 0) return FP8Q_OK;
-  if (!size_ok(tokens, hidden) || !size_ok(row_count, hidden)) return FP8Q_ERR_ARG;
+  if (hidden > FP8Q_MAX_HIDDEN || !size_ok(tokens, hidden) || !size_ok(row_count, hidden)) return FP8Q_ERR_ARG;
   const bool coded = format != FP8Q_ROWS_BF16;
   if (!slots || !out || (row_count && (!rows || (coded && !scales)))) return FP8Q_ERR_NULL;
   if (!aligned(rows, 16) || !aligned(out, 16) || !aligned(slots, 4) || !aligned(weights, 4) ||
@@ -232,6 +233,7 @@ fp8q_status fp8q_moe_combine_backward(const void *dy_bf16, const void *rows_bf16
                                       float *dweights_out, void *stream) {
   if (!pairs_ok(tokens, topk) || row_count > FP8Q_MAX_PAIRS) return FP8Q_ERR_ARG;
   if (tokens == 0) return FP8Q_OK;
+  if (hidden > FP8Q_MAX_HIDDEN) return FP8Q_ERR_ARG;
   if (hidden && (!size_ok(tokens, hidden) || !size_ok(row_count, hidden))) return FP8Q_ERR_ARG;
   if (!slots || !weights || !dweights_out) return FP8Q_ERR_NULL;
   if (hidden && (!dy_bf16 || (row_count && (!rows_bf16 || !drows_out)))) return FP8Q_ERR_NULL;

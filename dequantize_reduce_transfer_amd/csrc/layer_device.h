@@ -65,15 +65,19 @@ __device__ __forceinline__ float dpp_add(float v) {
   return v + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xF, 0xF, false));
 }
 
-// Sum over the wave, the same bits on every lane (each step adds the same two
-// numbers on both sides of an exchange).
+// Sum over the wave, the same bits on every lane: DPP steps inside the rows of
+// 16 (each adds the same two numbers on both sides of an exchange), then the
+// four rows' sums through scalar registers, with no LDS access to wait for.
 __device__ __forceinline__ float sum_wave(float v) {
   v = dpp_add<kDppQuadXor1>(v);
   v = dpp_add<kDppQuadXor2>(v);
   v = dpp_add<kDppRowHalfMirror>(v);
   v = dpp_add<kDppRowMirror>(v);
-  v += __shfl_xor(v, 16);
-  return v + __shfl_xor(v, 32);
+  const float a = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 0));
+  const float b = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 16));
+  const float c = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 32));
+  const float d = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 48));
+  return (a + b) + (c + d);
 }
 
 // v's elements moved down by n of `bits` bits each, zeros behind them.

@@ -87,6 +87,10 @@ struct MoePermute {
   uint64_t dst_rows;
   void *dst;
   void *dst_scales;
+  void advance(uint64_t n) {  // past the first n tokens
+    src = static_cast<const uint8_t *>(src) + n * row_bytes;
+    if (src_scales) src_scales = static_cast<const uint8_t *>(src_scales) + n * scale_row_bytes;
+  }
 };
 hipError_t launch_moe_permute(const MoePermute &a, hipStream_t stream);
 
@@ -101,6 +105,10 @@ struct MoeCombine {
   uint64_t hidden;
   void *out;
   bool out_bf16;
+  void advance(uint64_t n) {
+    if (weights) weights += n * topk;
+    out = static_cast<uint8_t *>(out) + n * hidden * (out_bf16 ? 2 : 4);
+  }
 };
 // format: the fp8q_row_format values.
 hipError_t launch_moe_combine(int format, const MoeCombine &a, hipStream_t stream);
@@ -116,6 +124,11 @@ struct MoeCombineBackward {
   uint64_t hidden;
   void *drows;
   float *dweights;
+  void advance(uint64_t n) {
+    dy = static_cast<const uint16_t *>(dy) + n * hidden;
+    weights += n * topk;
+    dweights += n * topk;
+  }
 };
 hipError_t launch_moe_combine_backward(const MoeCombineBackward &a, hipStream_t stream);
 

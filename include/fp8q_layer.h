@@ -35,6 +35,7 @@ extern "C" {
 #endif
 
 #define FP8Q_NORM_MAX_HIDDEN 32768   /* longest row of the norm entry points      */
+#define FP8Q_MAX_HIDDEN (((size_t)1) << 20) /* longest row of the moe entry points */
 #define FP8Q_MAX_TOPK 64             /* most experts a token                      */
 #define FP8Q_MAX_EXPERTS 1024        /* most experts                              */
 #define FP8Q_MAX_PAIRS (((size_t)1) << 30)  /* tokens * topk: pairs are int32     */
@@ -135,7 +136,8 @@ FP8Q_API fp8q_status fp8q_moe_sort(const void *ids, int id_bytes, size_t tokens,
  * The tokens' rows written to their places, scales alongside:
  *   dst[slots[t, j]] = src[t]      for every slot in [0, dst_rows)
  * Bytes are copied as they are, so rows may be of any type: row_bytes bytes
- * each, and scale_row_bytes bytes of scales (0 and NULL: none).  Each source
+ * each, and scale_row_bytes bytes of scales (0 and NULL: none; each at most
+ * 4 * FP8Q_MAX_HIDDEN).  Each source
  * row is read once, however many experts it goes to.  Rows of dst that no
  * slot names are not written; a slot outside [0, dst_rows) is skipped.
  *   src, src_scales  [tokens] rows of row_bytes / scale_row_bytes
