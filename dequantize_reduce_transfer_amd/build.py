@@ -32,6 +32,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB_PATH = os.path.join(PKG, "libfp8q.so")
 LAYER_LIB_PATH = os.path.join(PKG, "libfp8q_layer.so")
+BINDING_PATH = os.path.join(PKG, "_layer.so")       # the Python module over libfp8q_layer.so
 
 SOURCES = ["quantize.hip", "dequant_reduce.hip", "mx8_quantize.hip", "api.hip"]
 LAYER_SOURCES = ["rms_norm.hip", "moe_sort.hip", "moe_rows.hip", "layer_api.hip"]
@@ -63,17 +64,41 @@ def _link(objs, lib: str) -> None:
     os.replace(tmp, lib)
 
 
+def _build_binding() -> None:
+    """The Python module over libfp8q_layer.so (g++: host code only)."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+
+    tmp = BINDING_PATH + ".tmp%d" % os.getpid()
+    lib = os.path.join(os.path.dirname(os.path.abspath(torch.__file__)), "lib")
+    cmd = ["g++", "-std=c++17", "-O2", "-fPIC", "-shared", "-Wall", "-fvisibility=hidden",
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI), "-I", INCLUDE,
+           *["-isystem" + p for p in (*cpp_extension.include_paths(),
+                                      sysconfig.get_paths()["include"])],
+           os.path.join(CSRC, "layer_binding.cpp"), "-o", tmp, "-L", PKG, "-lfp8q_layer",
+           "-L", lib, "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("building the layer binding failed:\n%s\n%s" % (r.stdout, r.stderr))
+    os.replace(tmp, BINDING_PATH)
+
+
 def build(verbose: bool = False) -> str:
-    """Compile every HIP source and link both libraries (always rebuilds)."""
+    """Compile every HIP source, link both libraries, and build the Python
+    module over the second (always rebuilds)."""
     os.makedirs(BUILD_DIR, exist_ok=True)
     sources = [*SOURCES, *LAYER_SOURCES]
     with ThreadPoolExecutor(max_workers=min(len(sources), os.cpu_count() or 1)) as ex:
         objs = list(ex.map(_compile, sources))
     _link(objs[:len(SOURCES)], LIB_PATH)
     _link(objs[len(SOURCES):], LAYER_LIB_PATH)
+    _build_binding()
     if verbose:
         print("built", LIB_PATH)
         print("built", LAYER_LIB_PATH)
+        print("built", BINDING_PATH)
     return LIB_PATH
 
 
