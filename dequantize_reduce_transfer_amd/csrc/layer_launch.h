@@ -11,20 +11,14 @@
 
 namespace fp8q {
 
-// Workgroups of `waves` waves for `units` units of work, `per` a workgroup:
-// at most FP8Q_LAYER_MAX_WAVES waves (2^30 work-items, well inside the
-// dispatch packet's 32 bits); the kernels stride over what a grid does not
-// cover.
+// Workgroups of `waves` waves in one grid, at most: FP8Q_LAYER_MAX_WAVES waves
+// (2^30 work-items, well inside the dispatch packet's 32 bits).  Launchers
+// split what is more into several launches.
 #ifndef FP8Q_LAYER_MAX_WAVES
 #define FP8Q_LAYER_MAX_WAVES (1ull << 24)
 #endif
 constexpr uint64_t max_workgroups(uint32_t waves) {
   return FP8Q_LAYER_MAX_WAVES < waves ? 1 : FP8Q_LAYER_MAX_WAVES / waves;
-}
-inline uint32_t grid_for(uint64_t units, uint32_t per, uint32_t waves) {
-  const uint64_t most = max_workgroups(waves);
-  const uint64_t wgs = (units + per - 1) / per;
-  return (uint32_t)(wgs < 1 ? 1 : wgs < most ? wgs : most);
 }
 
 struct NormForward {

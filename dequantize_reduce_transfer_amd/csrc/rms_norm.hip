@@ -195,7 +195,7 @@ __global__ __launch_bounds__(64 * (W > 4 ? W : 4)) void norm_kernel(NormForward 
   }
 }
 
-// Launches over all rows, in grids of at most kMaxGrid workgroups.
+// Launches over all rows, in grids of at most max_workgroups.
 template <int OUT, bool RES, bool WB, Edge EDGE, int W, int V>
 hipError_t norm_launch(NormForward a, hipStream_t stream) {
   constexpr int kRows = W >= 4 ? 1 : 4 / W, kWgWaves = W > 4 ? W : 4;
