@@ -17,16 +17,17 @@
 // the buffers.
 //
 // Measured on MI355X at 16384 tokens, topk 8, hidden 2048 (median, rotating
-// inputs): permute of E4M3 rows with scales 55 us, 5.5 TB/s (a probe that
-// reads one stream and writes eight reaches 5.2); combine of bf16 rows 102
-// us, 5.9 TB/s, of E4M3 rows 55 us, 6.3 TB/s; combine's backward 207 us, 5.5
-// TB/s (a copy reaches 6.2-6.5).  What the choices are worth there: the four
-// waves of a workgroup side by side on one token's columns, so that whole 4
-// KiB rows move at once, 102 us against 136 with a wave a token; a wave's
-// eight rows in flight together 105 against 123 us one after another;
-// non-temporal row loads 105 against 112 us; four places a wave of the permute
-// 1% over eight and 7% over two, and its token rows loaded through the caches
-// 10% over non-temporal (the wave with the other four places reads them too).
+// inputs): permute of E4M3 rows with scales 52 us, 6.0 TB/s; combine of bf16
+// rows 102 us, 5.9 TB/s, of E4M3 rows 55 us, 6.3 TB/s; combine's backward 207
+// us, 5.5 TB/s (a plain copy reaches 6.2-6.5, one stream read and eight written
+// 5.2).  What the choices are worth there: the four waves of a workgroup side
+// by side on one token's columns, so that whole 4 KiB rows move at once, 102 us
+// against 136 with a wave a token; a wave's eight rows in flight together 105
+// against 123 us one after another; non-temporal row loads 105 against 112 us;
+// the permute's token rows loaded through the caches 10% over non-temporal (the
+// waves with the other places read them too).  Fewer rows in flight, other runs
+// of workgroups an XCD (8 to 256) and fewer resident workgroups all measured
+// within 1% or slower: what is left is scattered rows' share of HBM's rate.
 #include <type_traits>
 
 #include "fp8q_device.h"
@@ -38,7 +39,6 @@ namespace {
 
 constexpr int kWaves = 4;                      // waves a workgroup
 constexpr uint32_t kColumns = 8 * kWave;       // columns a wave covers with one vector a lane
-constexpr uint32_t kPermuteSlots = 4;          // places a wave of the permute writes to
 constexpr uint32_t kBackwardChoices = 8;       // choices a workgroup of the backward pass takes
 
 __device__ __forceinline__ uint32_t broadcast(uint32_t v, uint32_t from) {
@@ -104,11 +104,14 @@ __device__ __forceinline__ void copy_run(const uint8_t *src, uint8_t *dst, uint3
   }
 }
 
-// One wave a token, U KiB of its row (blockIdx.y) and kPermuteSlots of its
-// places (blockIdx.z); the wave that has the row's start has its scales too.
+// One wave a token, U KiB of its row (blockIdx.y) and `per` of its places
+// (`groups` waves side by side, so that what they all read comes from the
+// caches); the waves that have the row's start have its scales too.
 template <int U>
-__global__ __launch_bounds__(64 * kWaves) void permute_kernel(MoePermute a) {
-  const uint64_t t = (uint64_t)blockIdx.x * kWaves + uniform(threadIdx.x / kWave);
+__global__ __launch_bounds__(64 * kWaves) void permute_kernel(MoePermute a, uint32_t per, uint32_t groups) {
+  const uint32_t unit = blockIdx.x * kWaves + uniform(threadIdx.x / kWave);
+  const uint32_t group = unit % groups;
+  const uint64_t t = unit / groups;
   if (t >= a.tokens) return;
   const uint32_t lane = lane_id(), bytes = (uint32_t)a.row_bytes, sbytes = (uint32_t)a.scale_row_bytes;
   const uint32_t first = blockIdx.y * (1024 * U);
@@ -116,7 +119,7 @@ __global__ __launch_bounds__(64 * kWaves) void permute_kernel(MoePermute a) {
   const uint8_t *ssrc = static_cast<const uint8_t *>(a.src_scales) + t * sbytes;
   uint8_t *dst = static_cast<uint8_t *>(a.dst), *sdst = static_cast<uint8_t *>(a.dst_scales);
   const int slots = load_slots(a.slots, t, a.topk, a.dst_rows);
-  const bool lead = blockIdx.y == 0 && blockIdx.z == 0;
+  const bool lead = blockIdx.y == 0 && group == 0;
   if (bytes < 16) {
     if (lead) copy_run(src, dst, bytes, 0, slots, a.topk);
   } else {
@@ -135,8 +138,7 @@ __global__ __launch_bounds__(64 * kWaves) void permute_kernel(MoePermute a) {
     const uint32_t sat = sin ? vector_at(lane, sbytes) : 0;
     if (sin) s = load16<false>(ssrc + sat);
     loads_issued();
-    const uint32_t j0 = blockIdx.z * kPermuteSlots, left = a.topk - j0;
-    const uint32_t j1 = j0 + (left < kPermuteSlots ? left : kPermuteSlots);
+    const uint32_t j0 = group * per, left = a.topk - j0, j1 = j0 + (left < per ? left : per);
     for (uint32_t j = j0; j < j1; ++j) {
       const int slot = (int)broadcast((uint32_t)slots, j);
       if (slot < 0) continue;
@@ -380,14 +382,20 @@ hipError_t over_tokens(Args a, uint32_t pieces, Step &&step) {
 hipError_t launch_moe_permute(const MoePermute &a, hipStream_t stream) {
   const uint32_t kib = (uint32_t)((a.row_bytes + 1023) / 1024);
   const uint32_t U = kib <= 1 ? 1 : kib <= 2 ? 2 : 4;
-  return over_tokens(a, (kib + U - 1) / U, [&](const MoePermute &s) {
-    const dim3 grid((s.tokens + kWaves - 1) / kWaves, (kib + U - 1) / U, (s.topk + kPermuteSlots - 1) / kPermuteSlots), block(64 * kWaves);
+  // Places a wave writes to: one for rows of a KiB and more, so that as many
+  // waves as places store at once (16384 tokens, topk 8: 2 KiB rows 52.3 us
+  // against 56.2 with eight, 1 KiB rows 30.3 against 33.7); eight for shorter
+  // rows, where waves would be many and small (512 bytes 19.6 against 25.5, 256
+  // bytes 10.3 against 28.3), and for two choices (1 KiB rows 9.9 against 10.7).
+  const uint32_t per = a.row_bytes >= 1024 && a.topk > 2 ? 1 : 8, groups = (a.topk + per - 1) / per;
+  return over_tokens(a, (kib + U - 1) / U * groups, [&](const MoePermute &s) {
+    const dim3 grid((s.tokens * groups + kWaves - 1) / kWaves, (kib + U - 1) / U), block(64 * kWaves);
     if (U == 1)
-      hipLaunchKernelGGL((permute_kernel<1>), grid, block, 0, stream, s);
+      hipLaunchKernelGGL((permute_kernel<1>), grid, block, 0, stream, s, per, groups);
     else if (U == 2)
-      hipLaunchKernelGGL((permute_kernel<2>), grid, block, 0, stream, s);
+      hipLaunchKernelGGL((permute_kernel<2>), grid, block, 0, stream, s, per, groups);
     else
-      hipLaunchKernelGGL((permute_kernel<4>), grid, block, 0, stream, s);
+      hipLaunchKernelGGL((permute_kernel<4>), grid, block, 0, stream, s, per, groups);
   });
 }
 
