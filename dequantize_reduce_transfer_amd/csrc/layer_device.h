@@ -2,9 +2,9 @@
 //
 // Rows are [count, hidden] with no padding, so a row of an odd `hidden`
 // starts at any element.  Vectors of eight elements are therefore loaded and
-// stored through types that promise no alignment: gfx950 takes 16- and 8-byte global accesses at any byte address in one
-// instruction, and where the address is aligned they cost what the aligned
-// ones do.
+// stored through types that promise no alignment: gfx950 takes 16- and 8-byte
+// global accesses at any byte address in one instruction, and where the
+// address is aligned they cost what the aligned ones do.
 //
 // Column e of a vector may lie at or past the row's end: the loads below then
 // read inside the row all the same, and zeros are selected afterwards, so that

@@ -62,7 +62,9 @@ typedef enum {
  * fp32 scale per 128 elements) or of mx8_quantize (an E8M0 scale per 32),
  * applied to the fp32 values: the norm is taken of the unrounded sum, and y
  * is rounded once.  A block holding an inf or NaN gets the codec's NaN scale
- * and codes 0x7F.  rows == 0 or hidden == 0 is a successful no-op.
+ * and codes 0x7F.  A row whose sum of squares passes fp32's range has rstd 0; a
+ * row of zeros with eps 0 has rstd inf and y NaN.  rows == 0 or hidden == 0 is
+ * a successful no-op.
  *   x_bf16, residual_bf16  [rows, hidden]; residual NULL: none
  *   weight                 [hidden] fp32 or bf16
  *   eps                    finite, >= 0
