@@ -29,6 +29,7 @@ constexpr uint32_t kMaxExperts = 1024;         // FP8Q_MAX_EXPERTS
 constexpr uint32_t kNone = 0xFFFFFFFFu;
 constexpr int kSortWaves = 16;                 // of the large workgroups
 constexpr uint32_t kSortThreads = 64 * kSortWaves;
+static_assert(kSortThreads >= kMaxExperts, "a thread an expert adds up the counts and writes them");
 constexpr uint32_t kOneWorkgroup = 4096;       // pairs up to which one workgroup sorts
 
 // Pairs a workgroup takes in a sort by two kernels.  Each workgroup adds up
