@@ -113,7 +113,7 @@ __global__ __launch_bounds__(64 * W) void sort_place_kernel(const Id *ids, uint3
     if (e != kNone) atomicAdd(&mine[e], 1u);
     e = next;
   }
-  if (counts) {                                          // a thread adds up one expert's, every few workgroups'
+  if (W == kSortWaves && counts) {                       // a thread adds up one expert's, every few workgroups'
     const uint32_t x = tid & (lanes - 1);
     if (x < experts) {
       uint32_t all = 0, early = 0;
