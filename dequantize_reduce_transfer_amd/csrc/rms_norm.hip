@@ -32,7 +32,8 @@
 // in flight: 2048 waves measured best (16384 x 4096 with the residual's
 // gradient, 8 bytes an element: 87 us, 6.2 TB/s, with 256 workgroups of 8
 // waves; 89 with 512, 92 with 1024; 32768 x 2048 in 4-wave workgroups: 88 us
-// with 512, 112 with 256, 92 with 1024).
+// with 512, 112 with 256, 92 with 1024).  A few rows' gradients, which launches
+// bound, come from one kernel instead.
 #include "f32_encode.h"
 #include "fp8q_device.h"
 #include "layer_device.h"
@@ -253,12 +254,67 @@ struct BackwardRow {
   }
 };
 
+// The lane's part of sum(weight * dy * h) over the row; settles dy and h past
+// the row's end.
+template <Edge EDGE, int W, int V>
+__device__ __forceinline__ float backward_dot(BackwardRow<EDGE, W, V> &r, const float (&w)[V][8],
+                                              uint32_t tid, uint32_t hidden) {
+  float sum = 0.0f;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const uint32_t e = 8 * (v * 64 * W + tid);
+    float y[8], h[8];
+    r.dy[v] = take8_bf16<EDGE>(r.dy[v], e, hidden);
+    r.h[v] = take8_bf16<EDGE>(r.h[v], e, hidden);
+    widen8(r.dy[v], y);
+    widen8(r.h[v], h);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sum = __builtin_fmaf(y[j] * w[v][j], h[j], sum);
+  }
+  return sum;
+}
+
+// The lane's dx, with the row's sum.
+template <Edge EDGE, int W, int V>
+__device__ __forceinline__ void backward_dx(const NormBackward &a, const BackwardRow<EDGE, W, V> &r,
+                                            const float (&w)[V][8], float sum, uint64_t row,
+                                            uint32_t tid, bool live) {
+  const float c = sum * a.inv_hidden * r.rstd * r.rstd * r.rstd;
+  uint64_t base = row * (uint64_t)a.hidden;
+  asm volatile("" : "+s"(base));
+  uint16_t *dx = static_cast<uint16_t *>(a.dx) + base;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const uint32_t e = 8 * (v * 64 * W + tid);
+    float y[8], h[8], d[8];
+    widen8(r.dy[v], y);
+    widen8(r.h[v], h);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) d[j] = 0.0f;
+    if (a.dh) widen8(take8_bf16<EDGE>(r.dh[v], e, a.hidden), d);
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      d[j] = __builtin_fmaf(-h[j], c, __builtin_fmaf(y[j] * w[v][j], r.rstd, d[j]));
+    if (live && e < a.hidden) store8_bf16<EDGE, false>(dx, e, a.hidden, round8_bf16(d));
+  }
+}
+
+template <bool WB, Edge EDGE, int W, int V>
+__device__ __forceinline__ void backward_weights(const NormBackward &a, uint32_t tid, float (&w)[V][8]) {
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const uint32_t e = 8 * (v * 64 * W + tid);
+    Weights8<EDGE, WB> raw;
+    raw.load(a.weight, e, a.hidden);
+    raw.take(e, a.hidden, w[v]);
+  }
+}
+
 // W waves walk rows, each row's loads issued before the sum of the one
 // before; workgroups of max(W, 4) waves.  A workgroup's dweight sums go to
-// parts[blockIdx.x] (or, alone, to dweight itself).  The row sum's LDS slot
-// alternates, so one barrier a row is enough: a wave that is a row ahead
-// writes the other slot, and it can only be two ahead once every wave has
-// passed the barrier between.
+// parts[blockIdx.x].  The row sum's LDS slot alternates, so one barrier a row
+// is enough: a wave that is a row ahead writes the other slot, and it can only
+// be two ahead once every wave has passed the barrier between.
 template <bool WB, Edge EDGE, int W, int V>
 __global__ __launch_bounds__(64 * (W > 4 ? W : 4)) void norm_backward_kernel(NormBackward a, float *parts) {
   constexpr int kRows = W >= 4 ? 1 : 4 / W;              // rows a workgroup has in hand
@@ -272,55 +328,29 @@ __global__ __launch_bounds__(64 * (W > 4 ? W : 4)) void norm_backward_kernel(Nor
   BackwardRow<EDGE, W, V> next;
   next.load(a, row0 + sub < a.rows ? row0 + sub : row0, tid);
   float w[V][8], dw[V][8];
+  backward_weights<WB, EDGE, W>(a, tid, w);
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    const uint32_t e = 8 * (v * kThreads + tid);
-    Weights8<EDGE, WB> raw;
-    raw.load(a.weight, e, hidden);
-    raw.take(e, hidden, w[v]);
+  for (int v = 0; v < V; ++v)
 #pragma unroll
     for (int j = 0; j < 8; ++j) dw[v][j] = 0.0f;
-  }
   for (uint32_t turn = 0; row0 < a.rows; row0 += stride, turn ^= 1) {
     const bool live = row0 + sub < a.rows;               // the same for the row's waves
     BackwardRow<EDGE, W, V> cur = next;
     if (row0 + stride < a.rows)
       next.load(a, row0 + stride + sub < a.rows ? row0 + stride + sub : row0 + stride, tid);
-    float sum = 0.0f;
+    float sum = backward_dot(cur, w, tid, hidden);
+    if (live) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const uint32_t e = 8 * (v * kThreads + tid);
-      float y[8], h[8];
-      cur.dy[v] = take8_bf16<EDGE>(cur.dy[v], e, hidden);
-      cur.h[v] = take8_bf16<EDGE>(cur.h[v], e, hidden);
-      widen8(cur.dy[v], y);
-      widen8(cur.h[v], h);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) sum = __builtin_fmaf(y[j] * w[v][j], h[j], sum);
-      if (live) {
+      for (int v = 0; v < V; ++v) {
+        float y[8], h[8];
+        widen8(cur.dy[v], y);
+        widen8(cur.h[v], h);
 #pragma unroll
         for (int j = 0; j < 8; ++j) dw[v][j] = __builtin_fmaf(y[j], h[j] * cur.rstd, dw[v][j]);
       }
     }
     sum = sum_row<W>(sum, part[turn] + sub * W);
-    const float c = sum * a.inv_hidden * cur.rstd * cur.rstd * cur.rstd;
-    uint64_t base = (row0 + sub) * (uint64_t)hidden;
-    asm volatile("" : "+s"(base));
-    uint16_t *dx = static_cast<uint16_t *>(a.dx) + base;
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const uint32_t e = 8 * (v * kThreads + tid);
-      float y[8], h[8], d[8];
-      widen8(cur.dy[v], y);
-      widen8(cur.h[v], h);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) d[j] = 0.0f;
-      if (a.dh) widen8(take8_bf16<EDGE>(cur.dh[v], e, hidden), d);
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        d[j] = __builtin_fmaf(-h[j], c, __builtin_fmaf(y[j] * w[v][j], cur.rstd, d[j]));
-      if (live && e < hidden) store8_bf16<EDGE, false>(dx, e, hidden, round8_bf16(d));
-    }
+    backward_dx(a, cur, w, sum, row0 + sub, tid, live);
   }
   if constexpr (kRows > 1) {
     if (sub) {
@@ -339,14 +369,65 @@ __global__ __launch_bounds__(64 * (W > 4 ? W : 4)) void norm_backward_kernel(Nor
         for (int q = 0; q < kRows - 1; ++q) dw[v][j] += joined[((q * V + v) * 8 + j) * kThreads + tid];
   }
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
+  for (int v = 0; v < V; ++v) {                          // whole vectors, zeros past the row's end
     const uint32_t e = 8 * (v * kThreads + tid);
-    if (e >= hidden) continue;
-    if (parts)                                           // whole vectors, zeros past the row's end
+    if (e < hidden)
       store8_f32<kEven, false>(parts + (uint64_t)blockIdx.x * part_stride(hidden), e, hidden, dw[v]);
-    else
-      store8_f32<EDGE, false>(a.dweight, e, hidden, dw[v]);
   }
+}
+
+// Both gradients of a few rows in one launch: dweight does not need the rows'
+// sums, so the first `column_wgs` workgroups take 64 columns of all rows each,
+// and the rest the rows, one per W waves.  dy and h are read twice (the second
+// time from the caches), in no order: dx must not be dy.
+template <bool WB, Edge EDGE, int W, int V>
+__global__ __launch_bounds__(64 * (W > 4 ? W : 4)) void norm_backward_few_kernel(NormBackward a,
+                                                                                 uint32_t column_wgs) {
+  constexpr int kRows = W >= 4 ? 1 : 4 / W;
+  constexpr uint32_t kThreads = 64 * W;                  // threads a row
+  constexpr uint32_t kGroups = 8 * (W > 4 ? W : 4);      // rows at once of a column workgroup
+  __shared__ float part[kRows * W];
+  __shared__ float sums[kGroups][64];
+  const uint32_t hidden = a.hidden;
+  if (blockIdx.x < column_wgs) {
+    const uint32_t group = threadIdx.x / 8, c = 8 * (threadIdx.x % 8), e = blockIdx.x * 64 + c;
+    float dw[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) dw[j] = 0.0f;
+#pragma unroll 4
+    for (uint64_t row = group; row < a.rows; row += kGroups) {
+      const uint64_t base = row * (uint64_t)hidden;
+      const float rstd = a.rstd[row];
+      float y[8], h[8];
+      widen8(take8_bf16<EDGE>(load8_bf16<EDGE, false>(static_cast<const uint16_t *>(a.dy) + base, e, hidden),
+                              e, hidden), y);
+      widen8(take8_bf16<EDGE>(load8_bf16<EDGE, false>(static_cast<const uint16_t *>(a.h) + base, e, hidden),
+                              e, hidden), h);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) dw[j] = __builtin_fmaf(y[j], h[j] * rstd, dw[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sums[group][c + j] = dw[j];
+    __syncthreads();
+    const uint32_t column = blockIdx.x * 64 + threadIdx.x;
+    if (threadIdx.x < 64 && column < hidden) {
+      float t = sums[0][threadIdx.x];
+#pragma unroll 8
+      for (uint32_t g = 1; g < kGroups; ++g) t += sums[g][threadIdx.x];
+      a.dweight[column] = t;
+    }
+    return;
+  }
+  const uint32_t sub = W >= 4 ? 0 : uniform(threadIdx.x / kThreads);
+  const uint32_t tid = threadIdx.x % kThreads;
+  const uint64_t row0 = (uint64_t)(blockIdx.x - column_wgs) * kRows;
+  const bool live = row0 + sub < a.rows;                 // the same for the row's waves
+  BackwardRow<EDGE, W, V> row;
+  row.load(a, live ? row0 + sub : row0, tid);
+  float w[V][8];
+  backward_weights<WB, EDGE, W>(a, tid, w);
+  const float sum = sum_row<W>(backward_dot(row, w, tid, hidden), part + sub * W);
+  backward_dx(a, row, w, sum, row0 + sub, tid, live);
 }
 
 // dweight[e] = parts[0][e] + parts[1][e] + ...  A workgroup takes 64 columns,
@@ -392,12 +473,18 @@ constexpr BackwardShape backward_shape(uint32_t hidden) {
   return {1, hidden <= 2048 ? 512u : 256u};
 }
 
-// Up to kOneWorkgroupRows rows one workgroup walks them all and writes dweight
-// itself: no workspace and no second launch (in a graph, hidden 2048: 2.0 us
-// for one row and about 0.6 for each further one; two kernels take 4.3).
-constexpr uint64_t kOneWorkgroupRows = 4;
+// Up to 512 rows (and 2^22 elements) both gradients come from one launch.  On
+// MI355X in a graph, one launch against two: 1 row of 2048 2.3 against 4.3 us,
+// 256 rows 3.4 against 6.5, 509 rows of 2888 5.2 against 8.2, 509 of 8192 8.5
+// against 13.9; 1024 rows of 2888 12.4 against 10.1, 2048 of 512 9.2 against 6.8.
+// Where dx is dy itself it takes two: a row written would be missing from the
+// columns' sums.
+constexpr uint64_t kFewRows = 512, kFewElements = 1ull << 22;
+bool one_launch(const NormBackward &a) {
+  return a.rows == 0 || (a.rows <= kFewRows && a.rows * a.hidden <= kFewElements && a.dx != a.dy);
+}
+
 uint32_t backward_wgs(uint64_t rows, uint32_t hidden) {
-  if (rows <= kOneWorkgroupRows) return rows ? 1 : 0;
   const BackwardShape shape = backward_shape(hidden);
   const uint64_t wgs = (rows + shape.rows - 1) / shape.rows;
   return (uint32_t)(wgs < shape.most ? wgs : shape.most);
@@ -405,17 +492,20 @@ uint32_t backward_wgs(uint64_t rows, uint32_t hidden) {
 
 template <bool WB, Edge EDGE, int W, int V>
 hipError_t backward_launch(const NormBackward &a, hipStream_t stream) {
-  const uint32_t wgs = backward_wgs(a.rows, a.hidden);
-  float *parts = wgs > 1 ? a.workspace : nullptr;
-  if (wgs) {
-    hipLaunchKernelGGL((norm_backward_kernel<WB, EDGE, W, V>), dim3(wgs),
-                       dim3(64 * (W > 4 ? W : 4)), 0, stream, a, parts);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
+  constexpr uint32_t kRows = W >= 4 ? 1 : 4 / W;
+  const dim3 block(64 * (W > 4 ? W : 4));
+  if (one_launch(a)) {
+    const uint32_t columns = (a.hidden + 63) / 64;
+    hipLaunchKernelGGL((norm_backward_few_kernel<WB, EDGE, W, V>),
+                       dim3(columns + (uint32_t)((a.rows + kRows - 1) / kRows)), block, 0, stream, a, columns);
+    return hipGetLastError();
   }
-  if (wgs != 1)
-    hipLaunchKernelGGL(norm_parts_kernel, dim3((a.hidden + 63) / 64), dim3(64 * kPartWaves), 0,
-                       stream, parts, wgs, a.hidden, a.dweight);
+  const uint32_t wgs = backward_wgs(a.rows, a.hidden);
+  hipLaunchKernelGGL((norm_backward_kernel<WB, EDGE, W, V>), dim3(wgs), block, 0, stream, a, a.workspace);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(norm_parts_kernel, dim3((a.hidden + 63) / 64), dim3(64 * kPartWaves), 0, stream,
+                     a.workspace, wgs, a.hidden, a.dweight);
   return hipGetLastError();
 }
 
@@ -457,8 +547,7 @@ hipError_t launch_rms_norm(int out, const NormForward &a, hipStream_t stream) {
 }
 
 uint64_t norm_backward_workspace(uint64_t rows, uint32_t hidden) {
-  const uint32_t wgs = backward_wgs(rows, hidden);
-  return wgs > 1 ? 4ull * wgs * part_stride(hidden) : 0;
+  return 4ull * backward_wgs(rows, hidden) * part_stride(hidden);
 }
 
 hipError_t launch_rms_norm_backward(const NormBackward &a, hipStream_t stream) {

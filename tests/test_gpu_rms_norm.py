@@ -268,6 +268,37 @@ def test_norm_backward(hidden):
         check_grads(grads(dev, dyb, hb, w, kind, rstd, dhb), dyb, hb, w, rstd, dhb)
 
 
+@pytest.mark.parametrize("rows,hidden", [(512, 72), (513, 72), (512, 1), (700, 1), (515, 7), (512, 9), (600, 9),
+                                         (511, 513), (515, 513), (515, 1000), (512, 1411), (513, 1411),
+                                         (509, 2888), (515, 2888), (515, 6001), (512, 8192), (515, 8192),
+                                         (300, 16384), (515, 16384), (140, 32768), (515, 20000)])
+def test_norm_backward_either_side_of_one_launch(rows, hidden):
+    """Sizes around where one launch becomes two, at every way a row can end."""
+    dev = require_gpu()
+    rng = np.random.default_rng(rows + hidden)
+    hb, dyb = draw(rng, rows, hidden, 2.0), draw(rng, rows, hidden, 1e-2)
+    dhb = draw(rng, rows, hidden, 1e-2) if rows % 2 else None
+    w = weight(rng, hidden, "f32" if rows % 3 else "bf16")
+    kind = "f32" if rows % 3 else "bf16"
+    rstd = ref.rms_norm(bf16_bits_to_f32(hb), None, w, EPS)[1].astype(np.float32)
+    check_grads(grads(dev, dyb, hb, w, kind, rstd, dhb), dyb, hb, w, rstd, dhb)
+
+
+@pytest.mark.parametrize("in_place", ["dy", "dh"])
+@pytest.mark.parametrize("rows,hidden", [(1, 64), (3, 2048), (4, 9), (100, 513), (509, 2888), (512, 8192)])
+def test_norm_backward_few_rows_in_place(rows, hidden, in_place):
+    """dx over its own input: the weight's gradient still sees dy as it was."""
+    dev = require_gpu()
+    rng = np.random.default_rng(5 * rows + hidden)
+    hb, dyb, dhb = draw(rng, rows, hidden, 2.0), draw(rng, rows, hidden, 1e-2), draw(rng, rows, hidden, 1e-2)
+    w = weight(rng, hidden, "bf16")
+    rstd = ref.rms_norm(bf16_bits_to_f32(hb), None, w, EPS)[1].astype(np.float32)
+    got = grads(dev, dyb, hb, w, "bf16", rstd, dhb, in_place)
+    check_grads(got, dyb, hb, w, rstd, dhb)
+    again = grads(dev, dyb, hb, w, "bf16", rstd, dhb, in_place)
+    assert all(np.array_equal(x, y) for x, y in zip(got, again))
+
+
 @pytest.mark.parametrize("rows,hidden,in_place", [(1030, 512, "dh"), (2500, 1024, "dy"),
                                                   (1100, 2048, None), (1201, 4096, "dh"),
                                                   (5000, 72, None)])
