@@ -376,45 +376,79 @@ __global__ __launch_bounds__(64 * (W > 4 ? W : 4)) void norm_backward_kernel(Nor
   }
 }
 
+// dweight over the lane's columns [e, e + 8) of the rows first, first + STEP, ...,
+// DEPTH of them loaded at once.
+template <Edge EDGE, uint32_t STEP, uint32_t DEPTH>
+__device__ __forceinline__ void backward_columns(const NormBackward &a, uint32_t first, uint32_t e, float (&dw)[8]) {
+  const uint32_t hidden = a.hidden;
+  for (uint64_t row = first; row < a.rows; row += STEP * DEPTH) {
+    u32x4 dy[DEPTH], h[DEPTH];
+    float rstd[DEPTH];
+#pragma unroll
+    for (uint32_t k = 0; k < DEPTH; ++k) {
+      const uint64_t r = row + k * STEP < a.rows ? row + k * STEP : row;
+      dy[k] = load8_bf16<EDGE, false>(static_cast<const uint16_t *>(a.dy) + r * hidden, e, hidden);
+      h[k] = load8_bf16<EDGE, false>(static_cast<const uint16_t *>(a.h) + r * hidden, e, hidden);
+      rstd[k] = a.rstd[r];
+    }
+    loads_issued();
+#pragma unroll
+    for (uint32_t k = 0; k < DEPTH; ++k) {
+      if (row + k * STEP >= a.rows) break;
+      float y8[8], h8[8];
+      widen8(take8_bf16<EDGE>(dy[k], e, hidden), y8);
+      widen8(take8_bf16<EDGE>(h[k], e, hidden), h8);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) dw[j] = __builtin_fmaf(y8[j], h8[j] * rstd[k], dw[j]);
+    }
+  }
+}
+
+// Columns of a workgroup that sums them.  32 fill more of the chip, 64 are
+// whole cache lines and half as many workgroups in the rows' way: 509 rows of
+// 1000 3.0 us in a graph with 32, 4.0 with 64; 509 of 8192 11.5 and 8.2.
+constexpr uint32_t few_columns(int waves) { return waves <= 4 ? 32 : 64; }
+
 // Both gradients of a few rows in one launch: dweight does not need the rows'
-// sums, so the first `column_wgs` workgroups take 64 columns of all rows each,
+// sums, so the first `column_wgs` workgroups take few_columns of all rows each,
 // and the rest the rows, one per W waves.  dy and h are read twice (the second
-// time from the caches), in no order: dx must not be dy.
+// time from the caches), in no order: dx must not be dy.  Latency bounds it, so
+// a lane's rows are loaded 4 at a time, or 8 where there are more (509 rows of
+// 2888, read from HBM: 7.8 us with 8, 8.5 with 4; 200 rows 5.1 and 4.6), and
+// all threads add up the lanes' sums, 8 each and then the slices'.
 template <bool WB, Edge EDGE, int W, int V>
 __global__ __launch_bounds__(64 * (W > 4 ? W : 4)) void norm_backward_few_kernel(NormBackward a,
                                                                                  uint32_t column_wgs) {
   constexpr int kRows = W >= 4 ? 1 : 4 / W;
   constexpr uint32_t kThreads = 64 * W;                  // threads a row
-  constexpr uint32_t kGroups = 8 * (W > 4 ? W : 4);      // rows at once of a column workgroup
+  constexpr uint32_t kColumns = few_columns(W), kLanes = kColumns / 8;
+  constexpr uint32_t kGroups = 64 * (W > 4 ? W : 4) / kLanes, kSlices = kGroups / 8;
   __shared__ float part[kRows * W];
-  __shared__ float sums[kGroups][64];
+  __shared__ float sums[kGroups][kColumns], slices[kSlices][kColumns];
   const uint32_t hidden = a.hidden;
   if (blockIdx.x < column_wgs) {
-    const uint32_t group = threadIdx.x / 8, c = 8 * (threadIdx.x % 8), e = blockIdx.x * 64 + c;
+    const uint32_t group = threadIdx.x / kLanes, c = 8 * (threadIdx.x % kLanes);
+    const uint32_t first = blockIdx.x * kColumns;
     float dw[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) dw[j] = 0.0f;
-#pragma unroll 4
-    for (uint64_t row = group; row < a.rows; row += kGroups) {
-      const uint64_t base = row * (uint64_t)hidden;
-      const float rstd = a.rstd[row];
-      float y[8], h[8];
-      widen8(take8_bf16<EDGE>(load8_bf16<EDGE, false>(static_cast<const uint16_t *>(a.dy) + base, e, hidden),
-                              e, hidden), y);
-      widen8(take8_bf16<EDGE>(load8_bf16<EDGE, false>(static_cast<const uint16_t *>(a.h) + base, e, hidden),
-                              e, hidden), h);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) dw[j] = __builtin_fmaf(y[j], h[j] * rstd, dw[j]);
-    }
+    if (a.rows > 4 * kGroups)
+      backward_columns<EDGE, kGroups, 8>(a, group, first + c, dw);
+    else
+      backward_columns<EDGE, kGroups, 4>(a, group, first + c, dw);
 #pragma unroll
     for (int j = 0; j < 8; ++j) sums[group][c + j] = dw[j];
     __syncthreads();
-    const uint32_t column = blockIdx.x * 64 + threadIdx.x;
-    if (threadIdx.x < 64 && column < hidden) {
-      float t = sums[0][threadIdx.x];
-#pragma unroll 8
-      for (uint32_t g = 1; g < kGroups; ++g) t += sums[g][threadIdx.x];
-      a.dweight[column] = t;
+    const uint32_t column = threadIdx.x % kColumns, slice = threadIdx.x / kColumns;
+    float t = sums[8 * slice][column];
+#pragma unroll
+    for (uint32_t g = 1; g < 8; ++g) t += sums[8 * slice + g][column];
+    slices[slice][column] = t;
+    __syncthreads();
+    if (slice == 0 && first + column < hidden) {
+#pragma unroll
+      for (uint32_t g = 1; g < kSlices; ++g) t += slices[g][column];
+      a.dweight[first + column] = t;
     }
     return;
   }
@@ -473,15 +507,16 @@ constexpr BackwardShape backward_shape(uint32_t hidden) {
   return {1, hidden <= 2048 ? 512u : 256u};
 }
 
-// Up to 512 rows (and 2^22 elements) both gradients come from one launch.  On
-// MI355X in a graph, one launch against two: 1 row of 2048 2.3 against 4.3 us,
-// 256 rows 3.4 against 6.5, 509 rows of 2888 5.2 against 8.2, 509 of 8192 8.5
-// against 13.9; 1024 rows of 2888 12.4 against 10.1, 2048 of 512 9.2 against 6.8.
+// Up to 512 rows both gradients come from one launch.  On MI355X in a graph,
+// operands from HBM, one launch against two: 1 row of 2048 1.9 against 4.0 us,
+// 256 rows 4.4 against 7.0, 509 rows 7.0 against 10.9, 768 rows 10.1 against
+// 9.4; of 512 columns 3.8 against 5.0 (256 rows), 5.6 against 5.6 (509) and
+// 8.1 against 6.0 (768); of 16384 columns 18.8 against 26.6 (512).
 // Where dx is dy itself it takes two: a row written would be missing from the
 // columns' sums.
-constexpr uint64_t kFewRows = 512, kFewElements = 1ull << 22;
+constexpr uint64_t kFewRows = 512;
 bool one_launch(const NormBackward &a) {
-  return a.rows == 0 || (a.rows <= kFewRows && a.rows * a.hidden <= kFewElements && a.dx != a.dy);
+  return a.rows == 0 || (a.rows <= kFewRows && a.dx != a.dy);
 }
 
 uint32_t backward_wgs(uint64_t rows, uint32_t hidden) {
@@ -495,7 +530,7 @@ hipError_t backward_launch(const NormBackward &a, hipStream_t stream) {
   constexpr uint32_t kRows = W >= 4 ? 1 : 4 / W;
   const dim3 block(64 * (W > 4 ? W : 4));
   if (one_launch(a)) {
-    const uint32_t columns = (a.hidden + 63) / 64;
+    const uint32_t columns = (a.hidden + few_columns(W) - 1) / few_columns(W);
     hipLaunchKernelGGL((norm_backward_few_kernel<WB, EDGE, W, V>),
                        dim3(columns + (uint32_t)((a.rows + kRows - 1) / kRows)), block, 0, stream, a, columns);
     return hipGetLastError();
