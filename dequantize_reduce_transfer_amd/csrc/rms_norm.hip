@@ -32,8 +32,9 @@
 // in flight: 2048 waves measured best (16384 x 4096 with the residual's
 // gradient, 8 bytes an element: 87 us, 6.2 TB/s, with 256 workgroups of 8
 // waves; 89 with 512, 92 with 1024; 32768 x 2048 in 4-wave workgroups: 88 us
-// with 512, 112 with 256, 92 with 1024).  A few rows' gradients, which launches
-// bound, come from one kernel instead.
+// with 512, 112 with 256, 92 with 1024).  The gradients of a few rows, which
+// launches bound, and of very wide ones come from one kernel that reads dy and
+// h twice.
 #include "f32_encode.h"
 #include "fp8q_device.h"
 #include "layer_device.h"
@@ -407,21 +408,21 @@ __device__ __forceinline__ void backward_columns(const NormBackward &a, uint32_t
 // Columns of a workgroup that sums them.  32 fill more of the chip, 64 are
 // whole cache lines and half as many workgroups in the rows' way: 509 rows of
 // 1000 3.0 us in a graph with 32, 4.0 with 64; 509 of 8192 11.5 and 8.2.
-constexpr uint32_t few_columns(int waves) { return waves <= 4 ? 32 : 64; }
+constexpr uint32_t group_columns(int waves) { return waves <= 4 ? 32 : 64; }
 
-// Both gradients of a few rows in one launch: dweight does not need the rows'
-// sums, so the first `column_wgs` workgroups take few_columns of all rows each,
+// Both gradients in one launch: dweight does not need the rows'
+// sums, so the first `column_wgs` workgroups take group_columns of all rows each,
 // and the rest the rows, one per W waves.  dy and h are read twice (the second
 // time from the caches), in no order: dx must not be dy.  Latency bounds it, so
 // a lane's rows are loaded 4 at a time, or 8 where there are more (509 rows of
 // 2888, read from HBM: 7.8 us with 8, 8.5 with 4; 200 rows 5.1 and 4.6), and
 // all threads add up the lanes' sums, 8 each and then the slices'.
 template <bool WB, Edge EDGE, int W, int V>
-__global__ __launch_bounds__(64 * (W > 4 ? W : 4)) void norm_backward_few_kernel(NormBackward a,
+__global__ __launch_bounds__(64 * (W > 4 ? W : 4)) void norm_backward_columns_kernel(NormBackward a,
                                                                                  uint32_t column_wgs) {
   constexpr int kRows = W >= 4 ? 1 : 4 / W;
   constexpr uint32_t kThreads = 64 * W;                  // threads a row
-  constexpr uint32_t kColumns = few_columns(W), kLanes = kColumns / 8;
+  constexpr uint32_t kColumns = group_columns(W), kLanes = kColumns / 8;
   constexpr uint32_t kGroups = 64 * (W > 4 ? W : 4) / kLanes, kSlices = kGroups / 8;
   __shared__ float part[kRows * W];
   __shared__ float sums[kGroups][kColumns], slices[kSlices][kColumns];
@@ -514,27 +515,51 @@ constexpr BackwardShape backward_shape(uint32_t hidden) {
 // 8.1 against 6.0 (768); of 16384 columns 18.8 against 26.6 (512).
 // Where dx is dy itself it takes two: a row written would be missing from the
 // columns' sums.
+// Rows of more than 16384 always go this way, their dweight sums being too
+// many for the row kernel's registers: the second reading costs less than what
+// it spilled (4096 x 20000 188 us against 741, 4096 x 32768 310 against 831).
 constexpr uint64_t kFewRows = 512;
-bool one_launch(const NormBackward &a) {
-  return a.rows == 0 || (a.rows <= kFewRows && a.dx != a.dy);
+constexpr uint32_t kWideRow = 16384;
+bool by_columns(const NormBackward &a) {
+  return a.rows == 0 || a.hidden > kWideRow || (a.rows <= kFewRows && a.dx != a.dy);
 }
 
 uint32_t backward_wgs(uint64_t rows, uint32_t hidden) {
+  if (hidden > kWideRow) return 0;
   const BackwardShape shape = backward_shape(hidden);
   const uint64_t wgs = (rows + shape.rows - 1) / shape.rows;
   return (uint32_t)(wgs < shape.most ? wgs : shape.most);
 }
 
+// The columns and, unless dx is dy, rows in one grid; then what rows are left,
+// in grids of at most max_workgroups.
+template <bool WB, Edge EDGE, int W, int V>
+hipError_t columns_launch(NormBackward a, hipStream_t stream) {
+  constexpr uint32_t kRows = W >= 4 ? 1 : 4 / W, kWgWaves = W > 4 ? W : 4;
+  constexpr uint64_t kMost = max_workgroups(kWgWaves) * kRows;
+  uint32_t columns = (a.hidden + group_columns(W) - 1) / group_columns(W);
+  uint64_t rows = a.dx == a.dy ? 0 : a.rows < kMost ? a.rows : kMost;
+  for (;;) {
+    hipLaunchKernelGGL((norm_backward_columns_kernel<WB, EDGE, W, V>),
+                       dim3(columns + (uint32_t)((rows + kRows - 1) / kRows)), dim3(64 * kWgWaves), 0, stream, a,
+                       columns);
+    const uint64_t n = rows * a.hidden;
+    a.rows -= rows;
+    if (!a.rows) return hipGetLastError();
+    a.dy = static_cast<const uint16_t *>(a.dy) + n;
+    a.h = static_cast<const uint16_t *>(a.h) + n;
+    if (a.dh) a.dh = static_cast<const uint16_t *>(a.dh) + n;
+    a.rstd += rows;
+    a.dx = static_cast<uint16_t *>(a.dx) + n;
+    columns = 0;
+    rows = a.rows < kMost ? a.rows : kMost;
+  }
+}
+
 template <bool WB, Edge EDGE, int W, int V>
 hipError_t backward_launch(const NormBackward &a, hipStream_t stream) {
-  constexpr uint32_t kRows = W >= 4 ? 1 : 4 / W;
+  if (by_columns(a)) return columns_launch<WB, EDGE, W, V>(a, stream);
   const dim3 block(64 * (W > 4 ? W : 4));
-  if (one_launch(a)) {
-    const uint32_t columns = (a.hidden + few_columns(W) - 1) / few_columns(W);
-    hipLaunchKernelGGL((norm_backward_few_kernel<WB, EDGE, W, V>),
-                       dim3(columns + (uint32_t)((a.rows + kRows - 1) / kRows)), block, 0, stream, a, columns);
-    return hipGetLastError();
-  }
   const uint32_t wgs = backward_wgs(a.rows, a.hidden);
   hipLaunchKernelGGL((norm_backward_kernel<WB, EDGE, W, V>), dim3(wgs), block, 0, stream, a, a.workspace);
   const hipError_t e = hipGetLastError();
@@ -561,8 +586,8 @@ hipError_t backward_dispatch(const NormBackward &a, hipStream_t stream) {
   if (a.hidden <= 2048) return backward_launch<WB, EDGE, 4, 1>(a, stream);
   if (a.hidden <= 4096) return backward_launch<WB, EDGE, 8, 1>(a, stream);
   if (a.hidden <= 8192) return backward_launch<WB, EDGE, 8, 2>(a, stream);
-  if (a.hidden <= 16384) return backward_launch<WB, EDGE, 16, 2>(a, stream);
-  return backward_launch<WB, EDGE, 16, 4>(a, stream);
+  if (a.hidden <= kWideRow) return backward_launch<WB, EDGE, 16, 2>(a, stream);
+  return columns_launch<WB, EDGE, 16, 4>(a, stream);
 }
 
 template <bool WB>

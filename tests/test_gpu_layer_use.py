@@ -170,6 +170,33 @@ def test_offsets_past_32_bits():
 SMALL = os.path.join(HERE, "native", "libfp8q_layer_small_grid.so")
 
 
+@pytest.mark.parametrize("rows,hidden", [(100, 72), (333, 1030), (37, 8192), (9, 20000), (521, 16392)])
+@pytest.mark.parametrize("in_place", [None, "dy", "dh"])
+def test_split_norm_gradients_equal_whole_ones(rows, hidden, in_place):
+    dev = require_gpu()
+    if not os.path.exists(SMALL):
+        pytest.skip("the small-grid library is built by __graft_entry__.build()")
+    S = layer.layer_lib(SMALL)
+    g = torch.Generator(device=dev).manual_seed(rows * hidden)
+    dy, h, dh = (torch.randn(rows, hidden, generator=g, device=dev).bfloat16() for _ in range(3))
+    w = torch.rand(hidden, generator=g, device=dev)
+    rstd = torch.rand(rows, generator=g, device=dev) + 0.5
+    ws = torch.empty(fq.fp8q_rms_norm_backward_workspace(rows, hidden), dtype=torch.uint8, device=dev)
+    out = []
+    for lib in (layer.layer_lib(), S):
+        d = dict(dy=dy.clone(), dh=dh.clone())
+        dx = d[in_place] if in_place else torch.zeros_like(h)
+        dw = torch.zeros(hidden, device=dev)
+        torch.cuda.synchronize()
+        P = ctypes.c_void_p
+        assert lib.fp8q_rms_norm_backward(P(d["dy"].data_ptr()), P(h.data_ptr()), P(w.data_ptr()), 0,
+                                          P(rstd.data_ptr()), P(d["dh"].data_ptr()), rows, hidden, P(dx.data_ptr()),
+                                          P(dw.data_ptr()), P(ws.data_ptr() or None), ws.numel(), None) == 0
+        torch.cuda.synchronize()
+        out.append((dx, dw))
+    assert same(out[0][0], out[1][0]) and same(out[0][1], out[1][1])
+
+
 def test_split_launches_equal_whole_ones():
     """A build whose grids hold 64 waves splits every launch here; its outputs
     equal the library's bit for bit."""

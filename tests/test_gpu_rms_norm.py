@@ -284,6 +284,17 @@ def test_norm_backward_either_side_of_one_launch(rows, hidden):
     check_grads(grads(dev, dyb, hb, w, kind, rstd, dhb), dyb, hb, w, rstd, dhb)
 
 
+@pytest.mark.parametrize("in_place", [None, "dy", "dh"])
+@pytest.mark.parametrize("rows,hidden", [(1, 16392), (5, 32768), (700, 16385), (1300, 16392), (900, 20001)])
+def test_norm_backward_wide_rows(rows, hidden, in_place):
+    dev = require_gpu()
+    rng = np.random.default_rng(7 * rows + hidden)
+    hb, dyb, dhb = draw(rng, rows, hidden, 2.0), draw(rng, rows, hidden, 1e-2), draw(rng, rows, hidden, 1e-2)
+    w = weight(rng, hidden, "f32")
+    rstd = ref.rms_norm(bf16_bits_to_f32(hb), None, w, EPS)[1].astype(np.float32)
+    check_grads(grads(dev, dyb, hb, w, "f32", rstd, dhb, in_place), dyb, hb, w, rstd, dhb)
+
+
 @pytest.mark.parametrize("in_place", ["dy", "dh"])
 @pytest.mark.parametrize("rows,hidden", [(1, 64), (3, 2048), (4, 9), (100, 513), (509, 2888), (512, 8192)])
 def test_norm_backward_few_rows_in_place(rows, hidden, in_place):
