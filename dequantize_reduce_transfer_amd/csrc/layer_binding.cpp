@@ -10,7 +10,9 @@
 //
 // Every function returns (status, outputs...), with None for an output that is
 // neither given nor asked for, and raises TypeError or ValueError for a tensor
-// that does not fit.  The stream is the raw handle that layer.py passes.
+// that does not fit.  The stream is the raw handle that layer.py passes, of the
+// stream that is current during the call: torch's allocator takes memory from
+// the current stream's own, so what is allocated here is the kernels' alone.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
@@ -236,7 +238,7 @@ PyObject *rms_norm_quantize(PyObject *, PyObject *const *args, Py_ssize_t n) {
 }
 
 // dy, h, weight, rstd, dh, dx_out, dweight_out, workspace, stream
-// -> status, dx, dweight, workspace
+// -> status, dx, dweight
 PyObject *rms_norm_backward(PyObject *, PyObject *const *args, Py_ssize_t n) {
   return guarded([&] {
     Call c("fp8q_rms_norm_backward", args, n, 9);
@@ -260,12 +262,12 @@ PyObject *rms_norm_backward(PyObject *, PyObject *const *args, Py_ssize_t n) {
     const fp8q_status st = fp8q_rms_norm_backward(
         ptr(dy), ptr(h), ptr(w), (fp8q_weight_dtype)wcode, f32(rstd), ptr(dh), rows, hidden, ptr(dx),
         f32(dw), ptr(ws), ws.defined() ? ws.numel() : 0, c.stream(8));
-    return result(st, {dx, dw, ws});
+    return result(st, {dx, dw});
   });
 }
 
 // ids, experts, slots_out, pairs_out, offsets_out, workspace, stream
-// -> status, slots, pairs, offsets, workspace
+// -> status, slots, pairs, offsets
 PyObject *moe_sort(PyObject *, PyObject *const *args, Py_ssize_t n) {
   return guarded([&] {
     Call c("fp8q_moe_sort", args, n, 7);
@@ -285,7 +287,7 @@ PyObject *moe_sort(PyObject *, PyObject *const *args, Py_ssize_t n) {
     const fp8q_status st =
         fp8q_moe_sort(ptr(ids), (int)ids.element_size(), tokens, topk, (int)experts, i32(slots),
                       i32(pairs), i32(offsets), ptr(ws), ws.defined() ? ws.numel() : 0, c.stream(6));
-    return result(st, {slots, pairs, offsets, ws});
+    return result(st, {slots, pairs, offsets});
   });
 }
 

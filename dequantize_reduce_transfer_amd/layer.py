@@ -5,9 +5,10 @@ experts in the codec's formats, and brought back; the gradients that training
 needs are entry points of their own.  The C ABI and the formulas are in
 ``include/fp8q_layer.h``.  As with the codec's functions, tensors are checked
 (a TypeError or ValueError), outputs and workspaces are allocated with torch
-when the caller gives none, calls run on the current stream or on ``stream=``,
-and a non-zero status raises :class:`Fp8qError`; there is no CPU fallback.  The
-checks and allocations are in ``csrc/layer_binding.cpp``.
+when the caller gives none, calls run on the current stream or on ``stream=``
+(and allocate from that stream's memory), and a non-zero status raises
+:class:`Fp8qError`; there is no CPU fallback.  The checks and allocations are
+in ``csrc/layer_binding.cpp``.
 
   fp8q_rms_norm_quantize(x, weight, eps)      -> RmsNorm(q, scales, h, y, rstd)
   mx8_rms_norm_quantize(x, weight, eps)       -> RmsNorm(q, scales, h, y, rstd)
@@ -101,48 +102,51 @@ def _binding():
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _stream(t, stream) -> int:
-    """The raw handle of ``stream``, or of the current stream of t's GPU (0
-    where t is not on one: the call is refused for that)."""
-    if stream is not None:
-        return int(stream.cuda_stream)
-    if not (isinstance(t, torch.Tensor) and t.is_cuda):
-        return 0
-    if _raw_stream is not None:             # 0.1 us, against 2 for a Stream object
-        return _raw_stream(t.get_device())
-    return int(torch.cuda.current_stream(t.device).cuda_stream)
+def _call(what, function, t, args, stream):
+    """The binding's ``function`` on the current stream of t's GPU, or on the
+    stream that the caller named -> its outputs.
 
-
-def _named(stream, tensors) -> None:
-    """After a call on a stream that the caller named: every tensor recorded on
-    it, so that torch's allocator keeps their memory until it is done."""
-    for t in tensors:
-        if t is not None:
-            t.record_stream(stream)
-
-
-def _same_gpu(what: str, t, stream) -> None:
-    if isinstance(t, torch.Tensor) and t.is_cuda and stream.device != t.device:
+    A named stream is current while the binding allocates: outputs and
+    workspaces then come from that stream's own memory, which no work queued on
+    another stream still uses.  Every tensor of the call is recorded on it, so
+    that memory of other streams is kept until it is done, and the outputs on
+    the caller's stream, which is to read them and may release them before it
+    has."""
+    on_gpu = isinstance(t, torch.Tensor) and t.is_cuda          # if not, the call is refused for that
+    if stream is None:
+        if not on_gpu:
+            handle = 0
+        elif _raw_stream is not None:       # 0.1 us, against 2 for a Stream object
+            handle = _raw_stream(t.get_device())
+        else:
+            handle = int(torch.cuda.current_stream(t.device).cuda_stream)
+        status, *out = function(*args, handle)
+        if status:
+            _check(status, what)
+        return out
+    if on_gpu and stream.device != t.device:
         raise ValueError("%s: the stream is on %s, the tensors on %s" % (what, stream.device, t.device))
+    caller = torch.cuda.current_stream(stream.device)
+    with torch.cuda.device(stream.device):  # setting a stream makes its GPU current too
+        torch.cuda.set_stream(stream)       # 3 us less than torch.cuda.stream
+        try:
+            status, *out = function(*args, int(stream.cuda_stream))
+        finally:
+            torch.cuda.set_stream(caller)
+    for x in (*args, *out):
+        if isinstance(x, torch.Tensor):
+            x.record_stream(stream)
+    for x in out:
+        if x is not None:
+            x.record_stream(caller)
+    if status:
+        _check(status, what)
+    return out
 
 
 def row_scales(hidden: int) -> int:
     """fp32 scales of one row: one per 128 elements, the last block partial."""
     return (hidden + BLOCK - 1) // BLOCK
-
-
-def _norm(what, mx, x, weight, eps, residual, fmt, want_h, want_y, want_rstd, h_out, y_out, q_out,
-          scales_out, rstd_out, stream):
-    if stream is not None:
-        _same_gpu(what, x, stream)
-    status, *out = _binding().rms_norm_quantize(
-        mx, x, weight, eps, residual, fmt, want_h, want_y, want_rstd, h_out, y_out, q_out, scales_out,
-        rstd_out, _stream(x, stream))
-    if status:
-        _check(status, what)
-    if stream is not None:
-        _named(stream, [x, weight, residual, *out])
-    return RmsNorm._make(out)
 
 
 def fp8q_rms_norm_quantize(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
@@ -159,8 +163,9 @@ def fp8q_rms_norm_quantize(x: torch.Tensor, weight: torch.Tensor, eps: float = 1
     sum in bf16; ``h_out`` may be x or residual itself) comes with a residual,
     ``y`` (the normed rows in bf16) and ``rstd`` (fp32 [...]) when asked for.
     """
-    return _norm("fp8q_rms_norm_quantize", False, x, weight, eps, residual, fmt, want_h, want_y,
-                 want_rstd, h_out, y_out, q_out, scales_out, rstd_out, stream)
+    return RmsNorm._make(_call("fp8q_rms_norm_quantize", (_native or _binding()).rms_norm_quantize, x,
+                               (False, x, weight, eps, residual, fmt, want_h, want_y, want_rstd, h_out,
+                                y_out, q_out, scales_out, rstd_out), stream))
 
 
 def mx8_rms_norm_quantize(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
@@ -173,8 +178,9 @@ def mx8_rms_norm_quantize(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e
                           rstd_out: Optional[torch.Tensor] = None, stream=None) -> RmsNorm:
     """rms_norm(x + residual) * weight as MXFP8 rows (hidden a multiple of 32);
     otherwise as :func:`fp8q_rms_norm_quantize`."""
-    return _norm("mx8_rms_norm_quantize", True, x, weight, eps, residual, E4M3, want_h, want_y,
-                 want_rstd, h_out, y_out, q_out, e8m0_out, rstd_out, stream)
+    return RmsNorm._make(_call("mx8_rms_norm_quantize", (_native or _binding()).rms_norm_quantize, x,
+                               (True, x, weight, eps, residual, E4M3, want_h, want_y, want_rstd, h_out,
+                                y_out, q_out, e8m0_out, rstd_out), stream))
 
 
 def fp8q_rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor,
@@ -190,14 +196,8 @@ def fp8q_rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tens
     residual; ``dx_out`` may be dy or dh itself.  dweight is fp32 [hidden].
     ``workspace``: uint8, ``fp8q_rms_norm_backward_workspace`` bytes.
     """
-    if stream is not None:
-        _same_gpu("fp8q_rms_norm_backward", dy, stream)
-    status, dx, dw, ws = _binding().rms_norm_backward(dy, h, weight, rstd, dh, dx_out, dweight_out,
-                                                      workspace, _stream(dy, stream))
-    if status:
-        _check(status, "fp8q_rms_norm_backward")
-    if stream is not None:
-        _named(stream, [dy, h, weight, rstd, dh, dx, dw, ws])
+    dx, dw = _call("fp8q_rms_norm_backward", (_native or _binding()).rms_norm_backward, dy,
+                   (dy, h, weight, rstd, dh, dx_out, dweight_out, workspace), stream)
     return dx, dw
 
 
@@ -217,14 +217,8 @@ def fp8q_moe_sort(ids: torch.Tensor, experts: int, slots_out: Optional[torch.Ten
     [tokens * topk]: the pair at each place, -1 past the last; offsets int32
     [experts + 1]: each expert's first place, then their number.
     """
-    if stream is not None:
-        _same_gpu("fp8q_moe_sort", ids, stream)
-    status, slots, pairs, offsets, ws = _binding().moe_sort(ids, experts, slots_out, pairs_out,
-                                                            offsets_out, workspace, _stream(ids, stream))
-    if status:
-        _check(status, "fp8q_moe_sort")
-    if stream is not None:
-        _named(stream, [ids, slots, pairs, offsets, ws])
+    slots, pairs, offsets = _call("fp8q_moe_sort", (_native or _binding()).moe_sort, ids,
+                                  (ids, experts, slots_out, pairs_out, offsets_out, workspace), stream)
     return slots, pairs, offsets
 
 
@@ -243,14 +237,8 @@ def fp8q_moe_permute(x: torch.Tensor, slots: torch.Tensor, scales: Optional[torc
     when allocated here) and ``scales_out`` [rows, s]: rows no slot names are
     left as they are, slots outside the buffer are skipped.
     """
-    if stream is not None:
-        _same_gpu("fp8q_moe_permute", x, stream)
-    status, rows, rows_scales = _binding().moe_permute(x, slots, scales, out, scales_out,
-                                                       _stream(x, stream))
-    if status:
-        _check(status, "fp8q_moe_permute")
-    if stream is not None:
-        _named(stream, [x, slots, scales, rows, rows_scales])
+    rows, rows_scales = _call("fp8q_moe_permute", (_native or _binding()).moe_permute, x,
+                              (x, slots, scales, out, scales_out), stream)
     return rows, rows_scales
 
 
@@ -264,14 +252,8 @@ def fp8q_moe_combine(rows: torch.Tensor, slots: torch.Tensor, weights: Optional[
     [n, hidden / 32] (MXFP8).  weights fp32 [tokens, topk]; None sums the rows
     as they are, which for bf16 rows is the gradient of a permute.
     """
-    if stream is not None:
-        _same_gpu("fp8q_moe_combine", rows, stream)
-    status, y = _binding().moe_combine(rows, slots, weights, scales, fmt,
-                                       _out_code(out_dtype) == OUT_BF16, out, _stream(rows, stream))
-    if status:
-        _check(status, "fp8q_moe_combine")
-    if stream is not None:
-        _named(stream, [rows, slots, weights, scales, y])
+    (y,) = _call("fp8q_moe_combine", (_native or _binding()).moe_combine, rows,
+                 (rows, slots, weights, scales, fmt, _out_code(out_dtype) == OUT_BF16, out), stream)
     return y
 
 
@@ -281,12 +263,6 @@ def fp8q_moe_combine_backward(dy: torch.Tensor, rows: torch.Tensor, slots: torch
     """Gradients of a combine over bf16 rows -> (drows bf16 [n, hidden],
     dweights fp32 [tokens, topk]).  Rows of drows that no slot names are left
     as they are (an allocated one holds anything there)."""
-    if stream is not None:
-        _same_gpu("fp8q_moe_combine_backward", dy, stream)
-    status, drows, dweights = _binding().moe_combine_backward(dy, rows, slots, weights, drows_out,
-                                                              dweights_out, _stream(dy, stream))
-    if status:
-        _check(status, "fp8q_moe_combine_backward")
-    if stream is not None:
-        _named(stream, [dy, rows, slots, weights, drows, dweights])
+    drows, dweights = _call("fp8q_moe_combine_backward", (_native or _binding()).moe_combine_backward, dy,
+                            (dy, rows, slots, weights, drows_out, dweights_out), stream)
     return drows, dweights
