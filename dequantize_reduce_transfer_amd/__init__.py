@@ -108,7 +108,8 @@ def _run(what: str, tensors, fn, *args, stream=None) -> None:
     (the library launches on the current HIP device).  When the caller names
     a stream, every tensor is recorded on it, so that torch's caching
     allocator does not hand a tensor's memory to new work while the kernels
-    enqueued there may still read or write it."""
+    enqueued there may still read or write it (outputs that are allocated here
+    are that stream's already)."""
     dev = tensors[0].device
     for t in tensors[1:]:
         if t.device != dev:
@@ -126,6 +127,25 @@ def _stream(t: torch.Tensor, stream) -> int:
     if stream is None:
         stream = torch.cuda.current_stream(t.device)
     return int(stream.cuda_stream)
+
+
+def _empty(shape, dtype, like: torch.Tensor, stream) -> torch.Tensor:
+    """An output on like's GPU.  For a call on a stream that the caller names
+    it is that stream's own memory: a block that the current stream released
+    may have work pending there, which the named stream would not wait for.
+    It is recorded on the current stream, which is to read it and may release
+    it before it has."""
+    if stream is None or stream.device != like.device:        # the latter is refused
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    caller = torch.cuda.current_stream(like.device)
+    with torch.cuda.device(like.device):
+        torch.cuda.set_stream(stream)
+        try:
+            t = torch.empty(shape, dtype=dtype, device=like.device)
+        finally:
+            torch.cuda.set_stream(caller)
+    t.record_stream(caller)
+    return t
 
 
 def _need(t: torch.Tensor, dtype, name: str) -> None:
@@ -167,9 +187,9 @@ def fp8q_quantize(x: torch.Tensor, fmt: int = E4M3, q_out: Optional[torch.Tensor
     _need(x, torch.bfloat16, "x")
     n = x.numel()
     if q_out is None:
-        q_out = torch.empty(n, dtype=torch.uint8, device=x.device)
+        q_out = _empty(n, torch.uint8, x, stream)
     if scales_out is None:
-        scales_out = torch.empty(num_scales(n), dtype=torch.float32, device=x.device)
+        scales_out = _empty(num_scales(n), torch.float32, x, stream)
     _need(q_out, torch.uint8, "q_out")
     _need(scales_out, torch.float32, "scales_out")
     if q_out.numel() != n or scales_out.numel() != num_scales(n):
@@ -188,7 +208,7 @@ def fp8q_dequantize(q: torch.Tensor, scales: torch.Tensor, fmt: int = E4M3,
     if scales.numel() < num_scales(n):
         raise ValueError("scales must hold ceil(n/128) values")
     if out is None:
-        out = torch.empty(n, dtype=out_dtype, device=q.device)
+        out = _empty(n, out_dtype, q, stream)
     _need(out, out_dtype, "out")
     if out.numel() != n:
         raise ValueError("out must hold n values")
@@ -213,7 +233,7 @@ def fp8q_dequant_reduce(qs: Sequence[torch.Tensor], scales: Sequence[torch.Tenso
         if q.numel() != n or s.numel() < num_scales(n):
             raise ValueError("peer %d has the wrong size" % i)
     if out is None:
-        out = torch.empty(n, dtype=out_dtype, device=qs[0].device)
+        out = _empty(n, out_dtype, qs[0], stream)
     _need(out, out_dtype, "out")
     if out.numel() != n:
         raise ValueError("out must hold n values")
@@ -233,9 +253,9 @@ def mx8_quantize(w: torch.Tensor, q_out: Optional[torch.Tensor] = None,
         raise ValueError("K must be a multiple of 32")
     rows = w.numel() // K if K else 0
     if q_out is None:
-        q_out = torch.empty(w.shape, dtype=torch.uint8, device=w.device)
+        q_out = _empty(w.shape, torch.uint8, w, stream)
     if e8m0_out is None:
-        e8m0_out = torch.empty((rows, K // MX_BLOCK), dtype=torch.uint8, device=w.device)
+        e8m0_out = _empty((rows, K // MX_BLOCK), torch.uint8, w, stream)
     _need(q_out, torch.uint8, "q_out")
     _need(e8m0_out, torch.uint8, "e8m0_out")
     if q_out.numel() != w.numel() or e8m0_out.numel() != rows * (K // MX_BLOCK):
@@ -257,7 +277,7 @@ def fp8q_sum_f32(parts: Sequence[torch.Tensor], out_dtype=torch.float32,
         if p.numel() != n:
             raise ValueError("part %d has the wrong size" % i)
     if out is None:
-        out = torch.empty(n, dtype=out_dtype, device=parts[0].device)
+        out = _empty(n, out_dtype, parts[0], stream)
     _need(out, out_dtype, "out")
     if out.numel() != n:
         raise ValueError("out must hold n values")
@@ -283,9 +303,9 @@ def fp8q_dequant_reduce_requantize(qs: Sequence[torch.Tensor], scales: Sequence[
         if q.numel() != n or s.numel() < num_scales(n):
             raise ValueError("peer %d has the wrong size" % i)
     if q_out is None:
-        q_out = torch.empty(n, dtype=torch.uint8, device=qs[0].device)
+        q_out = _empty(n, torch.uint8, qs[0], stream)
     if scales_out is None:
-        scales_out = torch.empty(num_scales(n), dtype=torch.float32, device=qs[0].device)
+        scales_out = _empty(num_scales(n), torch.float32, qs[0], stream)
     _need(q_out, torch.uint8, "q_out")
     _need(scales_out, torch.float32, "scales_out")
     if q_out.numel() != n or scales_out.numel() != num_scales(n):
@@ -313,7 +333,7 @@ def mx8_dequant_reduce(qs: Sequence[torch.Tensor], e8m0s: Sequence[torch.Tensor]
         if q.shape != shape or e.numel() != rows * (K // MX_BLOCK):
             raise ValueError("peer %d has the wrong size" % i)
     if out is None:
-        out = torch.empty(shape, dtype=out_dtype, device=qs[0].device)
+        out = _empty(shape, out_dtype, qs[0], stream)
     _need(out, out_dtype, "out")
     if out.numel() != qs[0].numel():
         raise ValueError("out must hold rows * K values")
@@ -334,7 +354,7 @@ def mx8_dequantize(q: torch.Tensor, e8m0: torch.Tensor, out_dtype=torch.float32,
     if e8m0.numel() != rows * (K // MX_BLOCK):
         raise ValueError("e8m0 must hold rows * K / 32 bytes")
     if out is None:
-        out = torch.empty(q.shape, dtype=out_dtype, device=q.device)
+        out = _empty(q.shape, out_dtype, q, stream)
     _need(out, out_dtype, "out")
     if out.numel() != q.numel():
         raise ValueError("out must hold rows * K values")
@@ -349,9 +369,9 @@ def fp8q_quantize_tensorwise(x: torch.Tensor, fmt: int = E4M3, q_out: Optional[t
     _need(x, torch.bfloat16, "x")
     n = x.numel()
     if q_out is None:
-        q_out = torch.empty(n, dtype=torch.uint8, device=x.device)
+        q_out = _empty(n, torch.uint8, x, stream)
     if scale_out is None:
-        scale_out = torch.empty(1, dtype=torch.float32, device=x.device)
+        scale_out = _empty(1, torch.float32, x, stream)
     _need(q_out, torch.uint8, "q_out")
     _need(scale_out, torch.float32, "scale_out")
     if q_out.numel() != n or scale_out.numel() != 1:
