@@ -83,7 +83,14 @@ class Call {
     return v;
   }
 
-  bool truth(int i) const { return PyObject_IsTrue(args_[i]) > 0; }
+  bool truth(int i, const char *name) const {
+    const int v = PyObject_IsTrue(args_[i]);
+    if (v < 0) {
+      PyErr_Clear();
+      refuse_type(std::string(name) + " must be true or false");
+    }
+    return v > 0;
+  }
 
   void *stream(int i) const { return reinterpret_cast<void *>((intptr_t)integer(i, "stream")); }
 
@@ -202,8 +209,9 @@ fp8q_format format_code(const Call &c, int i) {
 // q_out, scales_out, rstd_out, stream -> status, q, scales, h, y, rstd
 PyObject *rms_norm_quantize(PyObject *, PyObject *const *args, Py_ssize_t n) {
   return guarded([&] {
-    const bool mx = n > 0 && PyObject_IsTrue(args[0]) > 0;
+    const bool mx = n > 0 && args[0] == Py_True;
     Call c(mx ? "mx8_rms_norm_quantize" : "fp8q_rms_norm_quantize", args, n, 15);
+    const bool want_h = c.truth(6, "want_h"), want_y = c.truth(7, "want_y"), want_rstd = c.truth(8, "want_rstd");
     const at::Tensor &x = c.tensor(1, "x", {at::kBFloat16});
     const int64_t hidden = hidden_of(x, "x"), rows = hidden ? x.numel() / hidden : 0;
     const at::Tensor &w = c.tensor(2, "weight", {at::kFloat, at::kBFloat16});
@@ -219,13 +227,13 @@ PyObject *rms_norm_quantize(PyObject *, PyObject *const *args, Py_ssize_t n) {
     const fp8q_format fmt = mx ? FP8Q_E4M3 : format_code(c, 5);
     if (mx && hidden % FP8Q_MX_BLOCK) refuse("hidden must be a multiple of 32");
     at::Tensor h, y, rstd;
-    if (res.defined() && (c.truth(6) || !c.absent(9))) h = c.output(9, "h_out", at::kBFloat16, x.sizes());
-    if (c.truth(7) || !c.absent(10)) y = c.output(10, "y_out", at::kBFloat16, x.sizes());
+    if (res.defined() && (want_h || !c.absent(9))) h = c.output(9, "h_out", at::kBFloat16, x.sizes());
+    if (want_y || !c.absent(10)) y = c.output(10, "y_out", at::kBFloat16, x.sizes());
     const at::Tensor q = c.output(11, "q_out", at::kByte, x.sizes());
     const at::Tensor s =
         mx ? c.output(12, "e8m0_out", at::kByte, {rows, hidden / FP8Q_MX_BLOCK})
            : c.output(12, "scales_out", at::kFloat, {rows, ceil_div(hidden, FP8Q_BLOCK)});
-    if (c.truth(8) || !c.absent(13))
+    if (want_rstd || !c.absent(13))
       rstd = c.output(13, "rstd_out", at::kFloat, x.sizes().slice(0, x.dim() - 1));
     const c10::DeviceGuard on(c.device());
     const fp8q_status st =
@@ -358,7 +366,7 @@ PyObject *moe_combine(PyObject *, PyObject *const *args, Py_ssize_t n) {
       if (scales.numel() != count * each)
         refuse("scales must hold " + std::to_string(each) + " values a row");
     }
-    const bool bf16 = c.truth(5);
+    const bool bf16 = c.truth(5, "out_dtype");
     const at::Tensor out =
         c.output(6, "out", bf16 ? at::kBFloat16 : at::kFloat, {slots.size(0), hidden});
     const c10::DeviceGuard on(c.device());

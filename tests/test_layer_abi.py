@@ -330,6 +330,14 @@ def test_binding_refuses_what_is_no_gpu_tensor_of_the_right_type():
         fq.fp8q_moe_combine(bf, i32, out_dtype=torch.float16)
 
 
+def test_a_flag_without_a_truth_value_is_refused():
+    bf, w = torch.zeros(2, 64, dtype=torch.bfloat16), torch.ones(64)
+    for flag in ("want_h", "want_y", "want_rstd"):
+        for norm in (fq.fp8q_rms_norm_quantize, fq.mx8_rms_norm_quantize):
+            with pytest.raises(TypeError, match=flag):
+                norm(bf, w, **{flag: torch.ones(2)})
+
+
 def test_missing_libraries_fail_loudly(monkeypatch, tmp_path):
     with pytest.raises(RuntimeError, match="not built"):
         layer.layer_lib(str(tmp_path / "absent.so"))
