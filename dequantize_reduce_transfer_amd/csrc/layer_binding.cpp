@@ -171,6 +171,17 @@ PyObject *result(fp8q_status status, std::initializer_list<at::Tensor> outputs) 
   return r;
 }
 
+// What torch raises where GPU memory runs out: a RuntimeError of its own, which
+// programs catch by that name.
+PyObject *out_of_memory_type() {
+  PyObject *torch = PyImport_ImportModule("torch");
+  PyObject *type = torch ? PyObject_GetAttrString(torch, "OutOfMemoryError") : nullptr;
+  Py_XDECREF(torch);
+  if (type) return type;
+  PyErr_Clear();
+  return Py_NewRef(PyExc_RuntimeError);
+}
+
 // Turns a refusal, and any C++ exception (an allocation that failed), into a
 // Python exception.
 template <typename Body>
@@ -180,7 +191,9 @@ PyObject *guarded(Body &&body) {
   } catch (const Refusal &r) {
     PyErr_SetString(r.type, r.text.c_str());
   } catch (const c10::OutOfMemoryError &e) {
-    PyErr_SetString(PyExc_MemoryError, e.what_without_backtrace());
+    PyObject *type = out_of_memory_type();
+    PyErr_SetString(type, e.what_without_backtrace());
+    Py_DECREF(type);
   } catch (const std::exception &e) {
     PyErr_SetString(PyExc_RuntimeError, e.what());
   }

@@ -313,6 +313,26 @@ def test_refusals():
             call()
 
 
+def test_memory_that_runs_out_raises_as_in_torch():
+    """An output that this process's limit of 2 GiB cannot hold: the exception
+    that torch's own allocations (and the codec's functions) raise, and the next
+    call goes through."""
+    dev = require_gpu()
+    torch.cuda.empty_cache()
+    x = torch.zeros(1 << 12, 1 << 14, dtype=torch.uint8, device=dev)
+    slots = torch.full((1 << 12, 64), -1, dtype=torch.int32, device=dev)
+    total = torch.cuda.get_device_properties(dev).total_memory
+    torch.cuda.set_per_process_memory_fraction((torch.cuda.memory_reserved(dev) + (2 << 30)) / total, dev)
+    try:
+        with pytest.raises(torch.OutOfMemoryError):
+            fq.fp8q_moe_permute(x, slots)              # 2^18 rows of 16 KiB: 4 GiB
+        rows, _ = fq.fp8q_moe_permute(x[:8], slots[:8])
+        torch.cuda.synchronize()
+        assert rows.shape == (512, 1 << 14)
+    finally:
+        torch.cuda.set_per_process_memory_fraction(1.0, dev)
+
+
 def test_unaligned_views_are_refused_and_strided_ones_too():
     dev = require_gpu()
     base = torch.zeros(4 * 64 + 8, dtype=torch.bfloat16, device=dev)
