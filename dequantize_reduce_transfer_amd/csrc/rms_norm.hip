@@ -275,12 +275,14 @@ __device__ __forceinline__ float backward_dot(BackwardRow<EDGE, W, V> &r, const 
   return sum;
 }
 
-// The lane's dx, with the row's sum.
+// The lane's dx, with the row's sum: (g - h * c) * rstd + dh, whose c is of the
+// order of g * rstd.  rstd^3 leaves fp32's range for rows whose dx is well
+// inside it.
 template <Edge EDGE, int W, int V>
 __device__ __forceinline__ void backward_dx(const NormBackward &a, const BackwardRow<EDGE, W, V> &r,
                                             const float (&w)[V][8], float sum, uint64_t row,
                                             uint32_t tid, bool live) {
-  const float c = sum * a.inv_hidden * r.rstd * r.rstd * r.rstd;
+  const float c = sum * a.inv_hidden * r.rstd * r.rstd;
   uint64_t base = row * (uint64_t)a.hidden;
   asm volatile("" : "+s"(base));
   uint16_t *dx = static_cast<uint16_t *>(a.dx) + base;
@@ -295,7 +297,7 @@ __device__ __forceinline__ void backward_dx(const NormBackward &a, const Backwar
     if (a.dh) widen8(take8_bf16<EDGE>(r.dh[v], e, a.hidden), d);
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      d[j] = __builtin_fmaf(-h[j], c, __builtin_fmaf(y[j] * w[v][j], r.rstd, d[j]));
+      d[j] = __builtin_fmaf(__builtin_fmaf(-h[j], c, y[j] * w[v][j]), r.rstd, d[j]);
     if (live && e < a.hidden) store8_bf16<EDGE, false>(dx, e, a.hidden, round8_bf16(d));
   }
 }

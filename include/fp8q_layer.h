@@ -92,9 +92,9 @@ FP8Q_API fp8q_status mx8_rms_norm_quantize(const void *x_bf16, const void *resid
  * The norm's backward pass, straight through the 8-bit rounding: with dy the
  * gradient of y and dh that of the residual stream past this point (NULL:
  * none), per row
- *   g  = weight * dy,   c = rstd^3 * sum(g * h) / hidden
- *   dx = g * rstd - h * c + dh          (x's and the residual's gradient)
- *   dweight = sum over the rows of dy * h * rstd
+ *   g  = weight * dy,   c = sum(g * h) / hidden * rstd^2
+ *   dx = (g - h * c) * rstd + dh        (x's and the residual's gradient)
+ *   dweight = sum over the rows of dy * (h * rstd)
  * in fp32, dx rounded once to bf16, dweight fp32.  The rows are summed in a
  * fixed order: the same call gives the same bits.  rows == 0 writes zeros to
  * dweight.  hidden == 0 is a no-op.

@@ -325,6 +325,21 @@ def test_norm_backward_many_rows(rows, hidden, in_place):
     assert all(np.array_equal(a, b) for a, b in zip(first, again)), "not the same bits twice"
 
 
+@pytest.mark.parametrize("rows,hidden", [(1, 64), (3, 2048), (700, 2048), (600, 513), (3, 20000)])
+@pytest.mark.parametrize("size,dy_size", [(1e-12, 1e-3), (1e-21, 1.0), (1e-25, 1e-3), (1e-33, 1e-2), (1e12, 1e-3),
+                                          (1e17, 1.0)])
+def test_norm_backward_of_rows_far_from_one(rows, hidden, size, dy_size):
+    """Rows whose rstd^3 leaves fp32's range, with gradients whose products with
+    them and whose dx are inside it."""
+    dev = require_gpu()
+    rng = np.random.default_rng(rows + hidden)
+    hb, dyb = draw(rng, rows, hidden, size), draw(rng, rows, hidden, dy_size)
+    w = weight(rng, hidden, "f32")
+    rstd = ref.rms_norm(bf16_bits_to_f32(hb), None, w, 0.0)[1].astype(np.float32)
+    assert np.isfinite(rstd).all() and (rstd > 0).all()
+    check_grads(grads(dev, dyb, hb, w, "f32", rstd, None), dyb, hb, w, rstd, None)
+
+
 def test_norm_backward_against_differences():
     """The device's gradients against central differences of the forward in
     64 bits, of loss = sum(dy * y) + sum(dh * h)."""
