@@ -62,9 +62,13 @@ typedef enum {
  * fp32 scale per 128 elements) or of mx8_quantize (an E8M0 scale per 32),
  * applied to the fp32 values: the norm is taken of the unrounded sum, and y
  * is rounded once.  A block holding an inf or NaN gets the codec's NaN scale
- * and codes 0x7F.  A row whose sum of squares passes fp32's range has rstd 0; a
- * row of zeros with eps 0 has rstd inf and y NaN.  rows == 0 or hidden == 0 is
- * a successful no-op.
+ * and codes 0x7F.  The sum of squares is held in fp32: a row where it passes
+ * fp32's range (values of about 1e19) has rstd 0; with eps 0, a row where it
+ * underflows to 0 (all values under 2^-75, about 2.6e-23, zeros included) has
+ * rstd inf, y inf or NaN (0 * inf), and so NaN scales, and one where it is
+ * subnormal (values under about 1e-19) an rstd of a subnormal's precision.
+ * Any eps from 1e-30 up is far from all of that at the small end.
+ * rows == 0 or hidden == 0 is a successful no-op.
  *   x_bf16, residual_bf16  [rows, hidden]; residual NULL: none
  *   weight                 [hidden] fp32 or bf16
  *   eps                    finite, >= 0

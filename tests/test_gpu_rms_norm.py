@@ -190,6 +190,31 @@ def test_norm_special_rows(fmt):
         assert_bf16_parity(y, f32_to_bf16_bits(y32), "y")
 
 
+@pytest.mark.parametrize("fmt", ["e4m3", "mx8"])
+def test_norm_at_the_small_end_of_the_sum_of_squares(fmt):
+    """Finite rows whose squares underflow in fp32: rstd inf, and no finite row
+    out of it, with eps 0; an ordinary rstd with a small eps.  A row just above
+    is normed as any other."""
+    dev = require_gpu()
+    hidden = 192
+    x = np.zeros((4, hidden), np.float32)
+    x[0] = 2.0 ** -76                          # squares of 2^-152 round to 0
+    x[1, 7] = 2.0 ** -80
+    x[2] = -(2.0 ** -100)
+    x[3] = 2.0 ** -60                          # squares of 2^-120
+    xb, w = f32_to_bf16_bits(x), np.ones(hidden, np.float32)
+    q, s, _, y, rstd = run(dev, FMTS[fmt], xb, None, w, "f32", eps=0.0)
+    assert np.isposinf(rstd[:3]).all() and abs(rstd[3] / 2.0 ** 60 - 1) <= RSTD_ROUNDINGS * ref.U32
+    y = bf16_bits_to_f32(y)
+    assert np.isposinf(y[0]).all() and np.isneginf(y[2]).all()
+    assert np.isposinf(y[1, 7]) and np.isnan(np.delete(y[1], 7)).all()
+    assert (q[:3] == 0x7F).all() and ((s[:3] == 255) if fmt == "mx8" else np.isnan(s[:3])).all()
+    eps = 2.0 ** -100                          # about 8e-31
+    got = run(dev, FMTS[fmt], xb, None, w, "f32", eps=eps)
+    assert (np.abs(got[4][:3] / 2.0 ** 50 - 1) <= RSTD_ROUNDINGS * ref.U32).all()
+    check(got, FMTS[fmt], xb, None, w, eps=eps)
+
+
 def test_norm_reads_back_through_the_codec():
     """With hidden a multiple of 128 the rows are the codec's flat layout."""
     dev = require_gpu()
