@@ -210,14 +210,17 @@ hipError_t norm_launch(NormForward a, hipStream_t stream) {
 
 template <int OUT, bool RES, bool WB, Edge EDGE>
 hipError_t norm_dispatch(const NormForward &a, hipStream_t stream) {
-  if constexpr (EDGE == kTiny) return norm_launch<OUT, RES, WB, kTiny, 1, 1>(a, stream);
-  if (a.hidden <= 512) return norm_launch<OUT, RES, WB, EDGE, 1, 1>(a, stream);
-  if (a.hidden <= 1024) return norm_launch<OUT, RES, WB, EDGE, 2, 1>(a, stream);
-  if (a.hidden <= 2048) return norm_launch<OUT, RES, WB, EDGE, 4, 1>(a, stream);
-  if (a.hidden <= 4096) return norm_launch<OUT, RES, WB, EDGE, 8, 1>(a, stream);
-  if (a.hidden <= 8192) return norm_launch<OUT, RES, WB, EDGE, 8, 2>(a, stream);
-  if (a.hidden <= 16384) return norm_launch<OUT, RES, WB, EDGE, 16, 2>(a, stream);
-  return norm_launch<OUT, RES, WB, EDGE, 16, 4>(a, stream);
+  if constexpr (EDGE == kTiny) {                         // hidden < 8: no other shape is built
+    return norm_launch<OUT, RES, WB, kTiny, 1, 1>(a, stream);
+  } else {
+    if (a.hidden <= 512) return norm_launch<OUT, RES, WB, EDGE, 1, 1>(a, stream);
+    if (a.hidden <= 1024) return norm_launch<OUT, RES, WB, EDGE, 2, 1>(a, stream);
+    if (a.hidden <= 2048) return norm_launch<OUT, RES, WB, EDGE, 4, 1>(a, stream);
+    if (a.hidden <= 4096) return norm_launch<OUT, RES, WB, EDGE, 8, 1>(a, stream);
+    if (a.hidden <= 8192) return norm_launch<OUT, RES, WB, EDGE, 8, 2>(a, stream);
+    if (a.hidden <= 16384) return norm_launch<OUT, RES, WB, EDGE, 16, 2>(a, stream);
+    return norm_launch<OUT, RES, WB, EDGE, 16, 4>(a, stream);
+  }
 }
 
 template <int OUT, Edge EDGE>
@@ -582,14 +585,17 @@ hipError_t norm_edges(const NormForward &a, hipStream_t stream) {
 
 template <bool WB, Edge EDGE>
 hipError_t backward_dispatch(const NormBackward &a, hipStream_t stream) {
-  if constexpr (EDGE == kTiny) return backward_launch<WB, kTiny, 1, 1>(a, stream);
-  if (a.hidden <= 512) return backward_launch<WB, EDGE, 1, 1>(a, stream);
-  if (a.hidden <= 1024) return backward_launch<WB, EDGE, 2, 1>(a, stream);
-  if (a.hidden <= 2048) return backward_launch<WB, EDGE, 4, 1>(a, stream);
-  if (a.hidden <= 4096) return backward_launch<WB, EDGE, 8, 1>(a, stream);
-  if (a.hidden <= 8192) return backward_launch<WB, EDGE, 8, 2>(a, stream);
-  if (a.hidden <= kWideRow) return backward_launch<WB, EDGE, 16, 2>(a, stream);
-  return columns_launch<WB, EDGE, 16, 4>(a, stream);
+  if constexpr (EDGE == kTiny) {
+    return backward_launch<WB, kTiny, 1, 1>(a, stream);
+  } else {
+    if (a.hidden <= 512) return backward_launch<WB, EDGE, 1, 1>(a, stream);
+    if (a.hidden <= 1024) return backward_launch<WB, EDGE, 2, 1>(a, stream);
+    if (a.hidden <= 2048) return backward_launch<WB, EDGE, 4, 1>(a, stream);
+    if (a.hidden <= 4096) return backward_launch<WB, EDGE, 8, 1>(a, stream);
+    if (a.hidden <= 8192) return backward_launch<WB, EDGE, 8, 2>(a, stream);
+    if (a.hidden <= kWideRow) return backward_launch<WB, EDGE, 16, 2>(a, stream);
+    return columns_launch<WB, EDGE, 16, 4>(a, stream);
+  }
 }
 
 template <bool WB>

@@ -71,6 +71,13 @@ def test_header_compiles_as_c():
     assert r.returncode == 0, r.stderr
 
 
+def test_library_holds_no_kernel_that_no_size_reaches():
+    """Rows of under eight elements (Edge 2) have one shape: a wave, a vector."""
+    names = re.findall(rb"\d+(norm\w*?_kernel)I\w*?LNS_4EdgeE2ELi(\d+)ELi(\d+)E", open(layer.LIB_PATH, "rb").read())
+    assert {(kernel.decode(), int(w), int(v)) for kernel, w, v in names} == {
+        (kernel, 1, 1) for kernel in ("norm_kernel", "norm_backward_kernel", "norm_backward_columns_kernel")}
+
+
 NORM = dict(x=0, res=1, w=2, wt=3, eps=4, rows=5, hidden=6, fmt=7, h=8, y=9, q=10, s=11, rstd=12)
 
 
