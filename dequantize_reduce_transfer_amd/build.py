@@ -1,5 +1,7 @@
 """Build the HIP libraries ``libfp8q.so`` (the codec) and ``libfp8q_layer.so``
-(the MoE layer's activation operators) in-tree for gfx950 with hipcc.
+(the MoE layer's activation operators) in-tree for gfx950 with hipcc, and then
+the Python module ``_layer.so`` over the second with g++ and torch's headers, a
+step of its own: where those do not fit, the libraries are built all the same.
 
     python -m dequantize_reduce_transfer_amd.build
 
@@ -64,8 +66,9 @@ def _link(objs, lib: str) -> None:
     os.replace(tmp, lib)
 
 
-def _build_binding() -> None:
-    """The Python module over libfp8q_layer.so (g++: host code only)."""
+def build_binding(verbose: bool = False) -> str:
+    """Compile the Python module over libfp8q_layer.so (g++: host code only),
+    which has to be built."""
     import sysconfig
 
     import torch
@@ -83,25 +86,27 @@ def _build_binding() -> None:
     if r.returncode != 0:
         raise RuntimeError("building the layer binding failed:\n%s\n%s" % (r.stdout, r.stderr))
     os.replace(tmp, BINDING_PATH)
+    if verbose:
+        print("built", BINDING_PATH)
+    return BINDING_PATH
 
 
 def build(verbose: bool = False) -> str:
-    """Compile every HIP source, link both libraries, and build the Python
-    module over the second (always rebuilds)."""
+    """Compile every HIP source and link both libraries (always rebuilds); needs
+    hipcc alone.  build_binding builds the Python module over the second."""
     os.makedirs(BUILD_DIR, exist_ok=True)
     sources = [*SOURCES, *LAYER_SOURCES]
     with ThreadPoolExecutor(max_workers=min(len(sources), os.cpu_count() or 1)) as ex:
         objs = list(ex.map(_compile, sources))
     _link(objs[:len(SOURCES)], LIB_PATH)
     _link(objs[len(SOURCES):], LAYER_LIB_PATH)
-    _build_binding()
     if verbose:
         print("built", LIB_PATH)
         print("built", LAYER_LIB_PATH)
-        print("built", BINDING_PATH)
     return LIB_PATH
 
 
 if __name__ == "__main__":
     build(verbose=True)
+    build_binding(verbose=True)
     sys.exit(0)

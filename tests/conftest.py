@@ -33,14 +33,24 @@ def _announce_gpu_case(request):
 
 @pytest.fixture(scope="session", autouse=True)
 def _built_libraries():
-    """Build the HIP library (hipcc, no GPU needed) and the oracle if either is
-    missing, so a fresh tree can run the suite; nothing is rebuilt otherwise."""
+    """Build the HIP libraries (hipcc, no GPU needed), the module over the layer
+    library and the oracle where one is missing, so a fresh tree can run the
+    suite; nothing is rebuilt otherwise.  A module that does not build fails the
+    tests that call it, and those alone."""
     import dequantize_reduce_transfer_amd as fq
     import oracle
+    from dequantize_reduce_transfer_amd import layer
 
     if not os.path.exists(fq.LIB_PATH) and not os.environ.get("FP8Q_LIB"):
         from dequantize_reduce_transfer_amd import build as hip_build
         sys.__stderr__.write("[conftest] building %s\n" % fq.LIB_PATH)
         hip_build.build()
+    if os.path.exists(layer.LIB_PATH) and not os.path.exists(layer.BINDING_PATH):
+        from dequantize_reduce_transfer_amd import build as hip_build
+        sys.__stderr__.write("[conftest] building %s\n" % layer.BINDING_PATH)
+        try:
+            hip_build.build_binding()
+        except (RuntimeError, OSError) as e:
+            sys.__stderr__.write("[conftest] %s\n" % e)
     oracle.build(force=False)
     yield
