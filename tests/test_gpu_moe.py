@@ -262,6 +262,30 @@ def test_combine_backward(hidden):
         assert (dw[slots < 0] == 0).all()
 
 
+@pytest.mark.parametrize("tokens,topk,hidden", [(1100, 8, 2048), (5000, 4, 72), (1301, 2, 1000), (2300, 1, 331)])
+def test_combine_and_its_gradient_in_large_grids(tokens, topk, hidden):
+    """More than 512 workgroups, and no multiple of that: from there on they take
+    tokens in runs an XCD, and the rest in their own order."""
+    dev = require_gpu()
+    rng = np.random.default_rng(tokens)
+    n = tokens * topk
+    slots = slot_table(rng, tokens, topk, n, 0.1)
+    weights = rng.random((tokens, topk)).astype(np.float32)
+    for fmt in ("bf16", "e4m3"):
+        rows, scales, values = rows_of(rng, n, hidden, fmt, dev)
+        check_combine(combine_on(dev, rows, scales, slots, weights, fmt, torch.float32), values, slots, weights,
+                      torch.float32)
+    rb = f32_to_bf16_bits(rng.standard_normal((n, hidden)).astype(np.float32))
+    dyb = f32_to_bf16_bits(rng.standard_normal((tokens, hidden)).astype(np.float32))
+    drows, dw = grads_on(dev, dyb, rb, slots, weights)
+    want, want_dw, mag = ref.combine_grads(bf16_bits_to_f32(dyb), bf16_bits_to_f32(rb), slots, weights)
+    named = ~np.isnan(want).any(1)
+    off = np.abs(bf16_bits_to_f32(drows)[named] - want[named])
+    assert (off <= (ref.U16 + 2 * ref.U32) * np.abs(want[named]) + ref.TINY16).all()
+    assert (drows[~named] == 0xA5A5).all(), "a row that no slot names was written"
+    assert (np.abs(dw - want_dw) <= (hidden + 6) * ref.U32 * mag).all()
+
+
 def test_combine_backward_against_differences():
     dev = require_gpu()
     rng = np.random.default_rng(8)
