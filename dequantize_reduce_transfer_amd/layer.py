@@ -120,27 +120,27 @@ def _call(what, function, t, args, stream):
             handle = _raw_stream(t.get_device())
         else:
             handle = int(torch.cuda.current_stream(t.device).cuda_stream)
-        status, *out = function(*args, handle)
-        if status:
-            _check(status, what)
-        return out
+        status_and_outputs = function(*args, handle)
+        if status_and_outputs[0]:
+            _check(status_and_outputs[0], what)
+        return status_and_outputs[1:]
     if on_gpu and stream.device != t.device:
         raise ValueError("%s: the stream is on %s, the tensors on %s" % (what, stream.device, t.device))
     caller = torch.cuda.current_stream(stream.device)
     with torch.cuda.device(stream.device):  # setting a stream makes its GPU current too
         torch.cuda.set_stream(stream)       # 3 us less than torch.cuda.stream
         try:
-            status, *out = function(*args, int(stream.cuda_stream))
+            status_and_outputs = function(*args, int(stream.cuda_stream))
         finally:
             torch.cuda.set_stream(caller)
+    out = status_and_outputs[1:]
     for x in (*args, *out):
         if isinstance(x, torch.Tensor):
             x.record_stream(stream)
     for x in out:
         if x is not None:
             x.record_stream(caller)
-    if status:
-        _check(status, what)
+    _check(status_and_outputs[0], what)
     return out
 
 
@@ -196,9 +196,8 @@ def fp8q_rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tens
     residual; ``dx_out`` may be dy or dh itself.  dweight is fp32 [hidden].
     ``workspace``: uint8, ``fp8q_rms_norm_backward_workspace`` bytes.
     """
-    dx, dw = _call("fp8q_rms_norm_backward", (_native or _binding()).rms_norm_backward, dy,
-                   (dy, h, weight, rstd, dh, dx_out, dweight_out, workspace), stream)
-    return dx, dw
+    return _call("fp8q_rms_norm_backward", (_native or _binding()).rms_norm_backward, dy,
+                 (dy, h, weight, rstd, dh, dx_out, dweight_out, workspace), stream)
 
 
 def fp8q_rms_norm_backward_workspace(rows: int, hidden: int) -> int:
@@ -217,9 +216,8 @@ def fp8q_moe_sort(ids: torch.Tensor, experts: int, slots_out: Optional[torch.Ten
     [tokens * topk]: the pair at each place, -1 past the last; offsets int32
     [experts + 1]: each expert's first place, then their number.
     """
-    slots, pairs, offsets = _call("fp8q_moe_sort", (_native or _binding()).moe_sort, ids,
-                                  (ids, experts, slots_out, pairs_out, offsets_out, workspace), stream)
-    return slots, pairs, offsets
+    return _call("fp8q_moe_sort", (_native or _binding()).moe_sort, ids,
+                 (ids, experts, slots_out, pairs_out, offsets_out, workspace), stream)
 
 
 def fp8q_moe_sort_workspace(tokens: int, topk: int, experts: int) -> int:
@@ -237,9 +235,8 @@ def fp8q_moe_permute(x: torch.Tensor, slots: torch.Tensor, scales: Optional[torc
     when allocated here) and ``scales_out`` [rows, s]: rows no slot names are
     left as they are, slots outside the buffer are skipped.
     """
-    rows, rows_scales = _call("fp8q_moe_permute", (_native or _binding()).moe_permute, x,
-                              (x, slots, scales, out, scales_out), stream)
-    return rows, rows_scales
+    return _call("fp8q_moe_permute", (_native or _binding()).moe_permute, x,
+                 (x, slots, scales, out, scales_out), stream)
 
 
 def fp8q_moe_combine(rows: torch.Tensor, slots: torch.Tensor, weights: Optional[torch.Tensor] = None,
@@ -252,9 +249,8 @@ def fp8q_moe_combine(rows: torch.Tensor, slots: torch.Tensor, weights: Optional[
     [n, hidden / 32] (MXFP8).  weights fp32 [tokens, topk]; None sums the rows
     as they are, which for bf16 rows is the gradient of a permute.
     """
-    (y,) = _call("fp8q_moe_combine", (_native or _binding()).moe_combine, rows,
-                 (rows, slots, weights, scales, fmt, _out_code(out_dtype) == OUT_BF16, out), stream)
-    return y
+    return _call("fp8q_moe_combine", (_native or _binding()).moe_combine, rows,
+                 (rows, slots, weights, scales, fmt, _out_code(out_dtype) == OUT_BF16, out), stream)[0]
 
 
 def fp8q_moe_combine_backward(dy: torch.Tensor, rows: torch.Tensor, slots: torch.Tensor,
@@ -263,6 +259,5 @@ def fp8q_moe_combine_backward(dy: torch.Tensor, rows: torch.Tensor, slots: torch
     """Gradients of a combine over bf16 rows -> (drows bf16 [n, hidden],
     dweights fp32 [tokens, topk]).  Rows of drows that no slot names are left
     as they are (an allocated one holds anything there)."""
-    drows, dweights = _call("fp8q_moe_combine_backward", (_native or _binding()).moe_combine_backward, dy,
-                            (dy, rows, slots, weights, drows_out, dweights_out), stream)
-    return drows, dweights
+    return _call("fp8q_moe_combine_backward", (_native or _binding()).moe_combine_backward, dy,
+                 (dy, rows, slots, weights, drows_out, dweights_out), stream)
