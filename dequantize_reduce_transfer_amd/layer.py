@@ -102,46 +102,49 @@ def _binding():
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _call(what, function, t, args, stream):
-    """The binding's ``function`` on the current stream of t's GPU, or on the
-    stream that the caller named -> its outputs.
+def _current(t) -> int:
+    """The raw handle of the current stream of t's GPU (0 where t is not on
+    one: the call is refused for that)."""
+    if not (isinstance(t, torch.Tensor) and t.is_cuda):
+        return 0
+    if _raw_stream is not None:             # 0.1 us, against 2 for a Stream object
+        return _raw_stream(t.get_device())
+    return int(torch.cuda.current_stream(t.device).cuda_stream)
 
-    A named stream is current while the binding allocates: outputs and
-    workspaces then come from that stream's own memory, which no work queued on
-    another stream still uses.  Every tensor of the call is recorded on it, so
-    that memory of other streams is kept until it is done, and the outputs on
-    the caller's stream, which is to read them and may release them before it
-    has."""
-    on_gpu = isinstance(t, torch.Tensor) and t.is_cuda          # if not, the call is refused for that
-    if stream is None:
-        if not on_gpu:
-            handle = 0
-        elif _raw_stream is not None:       # 0.1 us, against 2 for a Stream object
-            handle = _raw_stream(t.get_device())
-        else:
-            handle = int(torch.cuda.current_stream(t.device).cuda_stream)
-        status_and_outputs = function(*args, handle)
-        if status_and_outputs[0]:
-            _check(status_and_outputs[0], what)
-        return status_and_outputs[1:]
-    if on_gpu and stream.device != t.device:
+
+def _outputs(what: str, result):
+    """The outputs of the binding's (status, outputs...)."""
+    if result[0]:
+        _check(result[0], what)
+    return result[1:]
+
+
+def _on_stream(stream, what: str, function, t, *args):
+    """``function(t, *args)``, a call without a stream of its own, on the stream
+    that the caller named: it is current for the call.
+
+    Outputs and workspaces are allocated from the current stream's own memory,
+    so no work queued on another stream still uses them.  Every tensor of the
+    call is recorded on the named stream, so that memory of other streams is
+    kept until it is done, and the outputs on the caller's, which is to read
+    them and may release them before it has."""
+    if isinstance(t, torch.Tensor) and t.is_cuda and stream.device != t.device:
         raise ValueError("%s: the stream is on %s, the tensors on %s" % (what, stream.device, t.device))
     caller = torch.cuda.current_stream(stream.device)
     with torch.cuda.device(stream.device):  # setting a stream makes its GPU current too
         torch.cuda.set_stream(stream)       # 3 us less than torch.cuda.stream
         try:
-            status_and_outputs = function(*args, int(stream.cuda_stream))
+            result = function(t, *args)
         finally:
             torch.cuda.set_stream(caller)
-    out = status_and_outputs[1:]
-    for x in (*args, *out):
+    outputs = result if isinstance(result, tuple) else (result,)
+    for x in (t, *args, *outputs):
         if isinstance(x, torch.Tensor):
             x.record_stream(stream)
-    for x in out:
+    for x in outputs:
         if x is not None:
             x.record_stream(caller)
-    _check(status_and_outputs[0], what)
-    return out
+    return result
 
 
 def row_scales(hidden: int) -> int:
@@ -163,9 +166,12 @@ def fp8q_rms_norm_quantize(x: torch.Tensor, weight: torch.Tensor, eps: float = 1
     sum in bf16; ``h_out`` may be x or residual itself) comes with a residual,
     ``y`` (the normed rows in bf16) and ``rstd`` (fp32 [...]) when asked for.
     """
-    return RmsNorm._make(_call("fp8q_rms_norm_quantize", (_native or _binding()).rms_norm_quantize, x,
-                               (False, x, weight, eps, residual, fmt, want_h, want_y, want_rstd, h_out,
-                                y_out, q_out, scales_out, rstd_out), stream))
+    if stream is not None:
+        return _on_stream(stream, "fp8q_rms_norm_quantize", fp8q_rms_norm_quantize, x, weight, eps, residual,
+                          fmt, want_h, want_y, want_rstd, h_out, y_out, q_out, scales_out, rstd_out)
+    return RmsNorm._make(_outputs("fp8q_rms_norm_quantize", (_native or _binding()).rms_norm_quantize(
+        False, x, weight, eps, residual, fmt, want_h, want_y, want_rstd, h_out, y_out, q_out, scales_out,
+        rstd_out, _current(x))))
 
 
 def mx8_rms_norm_quantize(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
@@ -178,9 +184,12 @@ def mx8_rms_norm_quantize(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e
                           rstd_out: Optional[torch.Tensor] = None, stream=None) -> RmsNorm:
     """rms_norm(x + residual) * weight as MXFP8 rows (hidden a multiple of 32);
     otherwise as :func:`fp8q_rms_norm_quantize`."""
-    return RmsNorm._make(_call("mx8_rms_norm_quantize", (_native or _binding()).rms_norm_quantize, x,
-                               (True, x, weight, eps, residual, E4M3, want_h, want_y, want_rstd, h_out,
-                                y_out, q_out, e8m0_out, rstd_out), stream))
+    if stream is not None:
+        return _on_stream(stream, "mx8_rms_norm_quantize", mx8_rms_norm_quantize, x, weight, eps, residual,
+                          want_h, want_y, want_rstd, h_out, y_out, q_out, e8m0_out, rstd_out)
+    return RmsNorm._make(_outputs("mx8_rms_norm_quantize", (_native or _binding()).rms_norm_quantize(
+        True, x, weight, eps, residual, E4M3, want_h, want_y, want_rstd, h_out, y_out, q_out, e8m0_out,
+        rstd_out, _current(x))))
 
 
 def fp8q_rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor,
@@ -196,8 +205,11 @@ def fp8q_rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tens
     residual; ``dx_out`` may be dy or dh itself.  dweight is fp32 [hidden].
     ``workspace``: uint8, ``fp8q_rms_norm_backward_workspace`` bytes.
     """
-    return _call("fp8q_rms_norm_backward", (_native or _binding()).rms_norm_backward, dy,
-                 (dy, h, weight, rstd, dh, dx_out, dweight_out, workspace), stream)
+    if stream is not None:
+        return _on_stream(stream, "fp8q_rms_norm_backward", fp8q_rms_norm_backward, dy, h, weight, rstd, dh,
+                          dx_out, dweight_out, workspace)
+    return _outputs("fp8q_rms_norm_backward", (_native or _binding()).rms_norm_backward(
+        dy, h, weight, rstd, dh, dx_out, dweight_out, workspace, _current(dy)))
 
 
 def fp8q_rms_norm_backward_workspace(rows: int, hidden: int) -> int:
@@ -216,8 +228,11 @@ def fp8q_moe_sort(ids: torch.Tensor, experts: int, slots_out: Optional[torch.Ten
     [tokens * topk]: the pair at each place, -1 past the last; offsets int32
     [experts + 1]: each expert's first place, then their number.
     """
-    return _call("fp8q_moe_sort", (_native or _binding()).moe_sort, ids,
-                 (ids, experts, slots_out, pairs_out, offsets_out, workspace), stream)
+    if stream is not None:
+        return _on_stream(stream, "fp8q_moe_sort", fp8q_moe_sort, ids, experts, slots_out, pairs_out,
+                          offsets_out, workspace)
+    return _outputs("fp8q_moe_sort", (_native or _binding()).moe_sort(
+        ids, experts, slots_out, pairs_out, offsets_out, workspace, _current(ids)))
 
 
 def fp8q_moe_sort_workspace(tokens: int, topk: int, experts: int) -> int:
@@ -235,8 +250,10 @@ def fp8q_moe_permute(x: torch.Tensor, slots: torch.Tensor, scales: Optional[torc
     when allocated here) and ``scales_out`` [rows, s]: rows no slot names are
     left as they are, slots outside the buffer are skipped.
     """
-    return _call("fp8q_moe_permute", (_native or _binding()).moe_permute, x,
-                 (x, slots, scales, out, scales_out), stream)
+    if stream is not None:
+        return _on_stream(stream, "fp8q_moe_permute", fp8q_moe_permute, x, slots, scales, out, scales_out)
+    return _outputs("fp8q_moe_permute", (_native or _binding()).moe_permute(
+        x, slots, scales, out, scales_out, _current(x)))
 
 
 def fp8q_moe_combine(rows: torch.Tensor, slots: torch.Tensor, weights: Optional[torch.Tensor] = None,
@@ -249,8 +266,11 @@ def fp8q_moe_combine(rows: torch.Tensor, slots: torch.Tensor, weights: Optional[
     [n, hidden / 32] (MXFP8).  weights fp32 [tokens, topk]; None sums the rows
     as they are, which for bf16 rows is the gradient of a permute.
     """
-    return _call("fp8q_moe_combine", (_native or _binding()).moe_combine, rows,
-                 (rows, slots, weights, scales, fmt, _out_code(out_dtype) == OUT_BF16, out), stream)[0]
+    if stream is not None:
+        return _on_stream(stream, "fp8q_moe_combine", fp8q_moe_combine, rows, slots, weights, scales, fmt,
+                          out_dtype, out)
+    return _outputs("fp8q_moe_combine", (_native or _binding()).moe_combine(
+        rows, slots, weights, scales, fmt, _out_code(out_dtype) == OUT_BF16, out, _current(rows)))[0]
 
 
 def fp8q_moe_combine_backward(dy: torch.Tensor, rows: torch.Tensor, slots: torch.Tensor,
@@ -259,5 +279,8 @@ def fp8q_moe_combine_backward(dy: torch.Tensor, rows: torch.Tensor, slots: torch
     """Gradients of a combine over bf16 rows -> (drows bf16 [n, hidden],
     dweights fp32 [tokens, topk]).  Rows of drows that no slot names are left
     as they are (an allocated one holds anything there)."""
-    return _call("fp8q_moe_combine_backward", (_native or _binding()).moe_combine_backward, dy,
-                 (dy, rows, slots, weights, drows_out, dweights_out), stream)
+    if stream is not None:
+        return _on_stream(stream, "fp8q_moe_combine_backward", fp8q_moe_combine_backward, dy, rows, slots,
+                          weights, drows_out, dweights_out)
+    return _outputs("fp8q_moe_combine_backward", (_native or _binding()).moe_combine_backward(
+        dy, rows, slots, weights, drows_out, dweights_out, _current(dy)))

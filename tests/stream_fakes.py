@@ -4,6 +4,8 @@ import contextlib
 
 import torch
 
+from dequantize_reduce_transfer_amd import layer
+
 
 class FakeStream:
     def __init__(self, name, handle, device):
@@ -36,6 +38,7 @@ class FakeStreams:
         self.caller, self.named = FakeStream("caller", 1, device), FakeStream("named", 2, device)
         self.now = self.caller
         monkeypatch.setattr(torch.cuda, "current_stream", lambda d=None: self.now)
+        monkeypatch.setattr(layer, "_raw_stream", lambda index: self.now.cuda_stream)
         monkeypatch.setattr(torch.cuda, "set_stream", self._set)
         monkeypatch.setattr(torch.cuda, "stream", self._current)
         monkeypatch.setattr(torch.cuda, "device", lambda d: contextlib.nullcontext())
