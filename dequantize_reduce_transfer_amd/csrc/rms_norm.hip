@@ -520,9 +520,12 @@ constexpr BackwardShape backward_shape(uint32_t hidden) {
 // 8.1 against 6.0 (768); of 16384 columns 18.8 against 26.6 (512).
 // Where dx is dy itself it takes two: a row written would be missing from the
 // columns' sums.
-// Rows of more than 16384 always go this way, their dweight sums being too
+// Rows of more than 16384 always go this way, their dweight sums being far too
 // many for the row kernel's registers: the second reading costs less than what
 // it spilled (4096 x 20000 188 us against 741, 4096 x 32768 310 against 831).
+// Rows of 8193 to 16384 stay with the row kernel, which spills less there (16
+// registers a lane, 30 where hidden % 8 != 0): 4096 x 12288 99 us, 4096 x 16384
+// 119, 4096 x 16383 218, from HBM.
 constexpr uint64_t kFewRows = 512;
 constexpr uint32_t kWideRow = 16384;
 bool by_columns(const NormBackward &a) {

@@ -10,6 +10,11 @@ when the caller gives none, calls run on the current stream or on ``stream=``
 :class:`Fp8qError`; there is no CPU fallback.  The checks and allocations are
 in ``csrc/layer_binding.cpp``.
 
+Outputs carry no autograd history, also where an input requires a gradient: the
+gradients are the ``..._backward`` functions (and a combine without weights, for
+a permute's).  ``examples/moe_layer.py`` has the ``torch.autograd.Function``s
+that tie them together.
+
   fp8q_rms_norm_quantize(x, weight, eps)      -> RmsNorm(q, scales, h, y, rstd)
   mx8_rms_norm_quantize(x, weight, eps)       -> RmsNorm(q, scales, h, y, rstd)
   fp8q_rms_norm_backward(dy, h, weight, rstd) -> (dx bf16, dweight f32 [hidden])
@@ -165,6 +170,7 @@ def fp8q_rms_norm_quantize(x: torch.Tensor, weight: torch.Tensor, eps: float = 1
     x, residual bf16 [..., hidden]; weight fp32 or bf16 [hidden].  ``h`` (the
     sum in bf16; ``h_out`` may be x or residual itself) comes with a residual,
     ``y`` (the normed rows in bf16) and ``rstd`` (fp32 [...]) when asked for.
+    Not tracked by autograd: :func:`fp8q_rms_norm_backward` is the gradient.
     """
     if stream is not None:
         return _on_stream(stream, "fp8q_rms_norm_quantize", fp8q_rms_norm_quantize, x, weight, eps, residual,
@@ -248,7 +254,8 @@ def fp8q_moe_permute(x: torch.Tensor, slots: torch.Tensor, scales: Optional[torc
     x [tokens, hidden] of any dtype, scales [tokens, s] of any dtype or none;
     slots int32 [tokens, topk].  ``out`` [rows, hidden] (tokens * topk rows
     when allocated here) and ``scales_out`` [rows, s]: rows no slot names are
-    left as they are, slots outside the buffer are skipped.
+    left as they are, slots outside the buffer are skipped.  Not tracked by
+    autograd: :func:`fp8q_moe_combine` without weights is the gradient.
     """
     if stream is not None:
         return _on_stream(stream, "fp8q_moe_permute", fp8q_moe_permute, x, slots, scales, out, scales_out)
@@ -264,7 +271,8 @@ def fp8q_moe_combine(rows: torch.Tensor, slots: torch.Tensor, weights: Optional[
     rows [n, hidden]: bf16, or uint8 codes with their ``scales``: fp32
     [n, ceil(hidden / 128)] (``fmt`` E4M3 or E5M2), or uint8 E8M0
     [n, hidden / 32] (MXFP8).  weights fp32 [tokens, topk]; None sums the rows
-    as they are, which for bf16 rows is the gradient of a permute.
+    as they are, which for bf16 rows is the gradient of a permute.  Not tracked
+    by autograd: :func:`fp8q_moe_combine_backward` is the gradient, of bf16 rows.
     """
     if stream is not None:
         return _on_stream(stream, "fp8q_moe_combine", fp8q_moe_combine, rows, slots, weights, scales, fmt,
@@ -278,7 +286,8 @@ def fp8q_moe_combine_backward(dy: torch.Tensor, rows: torch.Tensor, slots: torch
                               dweights_out: Optional[torch.Tensor] = None, stream=None):
     """Gradients of a combine over bf16 rows -> (drows bf16 [n, hidden],
     dweights fp32 [tokens, topk]).  Rows of drows that no slot names are left
-    as they are (an allocated one holds anything there)."""
+    as they are (an allocated one holds anything there).  Rows that were combined
+    from codes are dequantized for it first."""
     if stream is not None:
         return _on_stream(stream, "fp8q_moe_combine_backward", fp8q_moe_combine_backward, dy, rows, slots,
                           weights, drows_out, dweights_out)

@@ -177,7 +177,7 @@ FP8Q_API fp8q_status fp8q_moe_combine(const void *rows, fp8q_row_format format, 
 
 /*
  * The gradients of fp8q_moe_combine over bf16 rows: for every slot s = slots[t, j]
- * in [0, row_count)
+ * in [0, row_count) (rows in 8 bits are to be dequantized first)
  *   drows[s] = weights[t, j] * dy[t]                 (fp32, rounded once)
  *   dweights[t, j] = sum over hidden of dy[t] * rows[s]
  * and dweights[t, j] = 0 for every other slot.  Rows of drows that no slot
