@@ -20,7 +20,10 @@ Functions (same names as the C entry points):
 
 The MoE layer's activation operators (norm into 8 bits, rows to their experts
 and back, their gradients) are those of ``layer.py``, over ``libfp8q_layer.so``
-and ``include/fp8q_layer.h``; they are names of this package too.
+and ``include/fp8q_layer.h``; they are names of this package too.  So are the
+model's operators on both ends of the wire (routing, an MoE layer served from
+quantized weights, gradient norm and clipping), those of ``model.py``, over
+``libfp8q_model.so`` and ``include/fp8q_model.h``.
 """
 from __future__ import annotations
 
@@ -385,3 +388,5 @@ from .layer import (RmsNorm, fp8q_moe_combine, fp8q_moe_combine_backward,  # noq
                     fp8q_moe_permute, fp8q_moe_sort, fp8q_moe_sort_workspace,
                     fp8q_rms_norm_backward, fp8q_rms_norm_backward_workspace,
                     fp8q_rms_norm_quantize, mx8_rms_norm_quantize)
+from .model import (fp8q_grad_clip, fp8q_grad_sumsq, fp8q_moe_experts,  # noqa: E402,F401
+                    fp8q_moe_experts_workspace, fp8q_moe_route, fp8q_moe_route_backward)

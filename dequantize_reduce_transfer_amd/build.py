@@ -1,7 +1,9 @@
-"""Build the HIP libraries ``libfp8q.so`` (the codec) and ``libfp8q_layer.so``
-(the MoE layer's activation operators) in-tree for gfx950 with hipcc, and then
-the Python module ``_layer.so`` over the second with g++ and torch's headers, a
-step of its own: where those do not fit, the libraries are built all the same.
+"""Build the HIP libraries ``libfp8q.so`` (the codec), ``libfp8q_layer.so`` (the
+MoE layer's activation operators) and ``libfp8q_model.so`` (the model's operators
+on both ends of the wire) in-tree for gfx950 with hipcc, and then the Python
+modules ``_layer.so`` and ``_model.so`` over the last two with g++ and torch's
+headers, steps of their own: where those do not fit, the libraries are built all
+the same.
 
     python -m dequantize_reduce_transfer_amd.build
 
@@ -35,9 +37,12 @@ BUILD_DIR = os.path.join(ROOT, "_build")
 LIB_PATH = os.path.join(PKG, "libfp8q.so")
 LAYER_LIB_PATH = os.path.join(PKG, "libfp8q_layer.so")
 BINDING_PATH = os.path.join(PKG, "_layer.so")       # the Python module over libfp8q_layer.so
+MODEL_LIB_PATH = os.path.join(PKG, "libfp8q_model.so")
+MODEL_BINDING_PATH = os.path.join(PKG, "_model.so")  # the Python module over libfp8q_model.so
 
 SOURCES = ["quantize.hip", "dequant_reduce.hip", "mx8_quantize.hip", "api.hip"]
 LAYER_SOURCES = ["rms_norm.hip", "moe_sort.hip", "moe_rows.hip", "layer_api.hip"]
+MODEL_SOURCES = ["moe_route.hip", "moe_experts.hip", "grad_clip.hip", "model_api.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 CXXFLAGS = [
@@ -57,6 +62,12 @@ def _compile(src: str) -> str:
     return obj
 
 
+def _compile_all(sources):
+    os.makedirs(BUILD_DIR, exist_ok=True)
+    with ThreadPoolExecutor(max_workers=min(len(sources), os.cpu_count() or 1)) as ex:
+        return list(ex.map(_compile, sources))
+
+
 def _link(objs, lib: str) -> None:
     tmp = lib + ".tmp%d" % os.getpid()
     cmd = [HIPCC, "--offload-arch=" + ARCH, "-shared", "-fPIC", "-o", tmp, *objs]
@@ -66,38 +77,46 @@ def _link(objs, lib: str) -> None:
     os.replace(tmp, lib)
 
 
-def build_binding(verbose: bool = False) -> str:
-    """Compile the Python module over libfp8q_layer.so (g++: host code only),
+def _build_module(source: str, library: str, path: str, verbose: bool) -> str:
+    """Compile a Python module over one of the libraries (g++: host code only),
     which has to be built."""
     import sysconfig
 
     import torch
     from torch.utils import cpp_extension
 
-    tmp = BINDING_PATH + ".tmp%d" % os.getpid()
+    tmp = path + ".tmp%d" % os.getpid()
     lib = os.path.join(os.path.dirname(os.path.abspath(torch.__file__)), "lib")
     cmd = ["g++", "-std=c++17", "-O2", "-fPIC", "-shared", "-Wall", "-fvisibility=hidden",
            "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI), "-I", INCLUDE,
            *["-isystem" + p for p in (*cpp_extension.include_paths(),
                                       sysconfig.get_paths()["include"])],
-           os.path.join(CSRC, "layer_binding.cpp"), "-o", tmp, "-L", PKG, "-lfp8q_layer",
+           os.path.join(CSRC, source), "-o", tmp, "-L", PKG, "-l" + library,
            "-L", lib, "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-Wl,-rpath,$ORIGIN"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError("building the layer binding failed:\n%s\n%s" % (r.stdout, r.stderr))
-    os.replace(tmp, BINDING_PATH)
+        raise RuntimeError("building %s failed:\n%s\n%s" % (os.path.basename(path), r.stdout, r.stderr))
+    os.replace(tmp, path)
     if verbose:
-        print("built", BINDING_PATH)
-    return BINDING_PATH
+        print("built", path)
+    return path
+
+
+def build_binding(verbose: bool = False) -> str:
+    """Compile the Python module over libfp8q_layer.so, which has to be built."""
+    return _build_module("layer_binding.cpp", "fp8q_layer", BINDING_PATH, verbose)
+
+
+def build_model_binding(verbose: bool = False) -> str:
+    """Compile the Python module over libfp8q_model.so, which has to be built."""
+    return _build_module("model_binding.cpp", "fp8q_model", MODEL_BINDING_PATH, verbose)
 
 
 def build(verbose: bool = False) -> str:
-    """Compile every HIP source and link both libraries (always rebuilds); needs
-    hipcc alone.  build_binding builds the Python module over the second."""
-    os.makedirs(BUILD_DIR, exist_ok=True)
-    sources = [*SOURCES, *LAYER_SOURCES]
-    with ThreadPoolExecutor(max_workers=min(len(sources), os.cpu_count() or 1)) as ex:
-        objs = list(ex.map(_compile, sources))
+    """Compile the codec's and the layer's HIP sources and link both libraries
+    (always rebuilds); needs hipcc alone.  build_binding builds the Python module
+    over the second."""
+    objs = _compile_all([*SOURCES, *LAYER_SOURCES])
     _link(objs[:len(SOURCES)], LIB_PATH)
     _link(objs[len(SOURCES):], LAYER_LIB_PATH)
     if verbose:
@@ -106,7 +125,18 @@ def build(verbose: bool = False) -> str:
     return LIB_PATH
 
 
+def build_model(verbose: bool = False) -> str:
+    """Compile and link libfp8q_model.so (always rebuilds); needs hipcc alone.
+    build_model_binding builds the Python module over it."""
+    _link(_compile_all(MODEL_SOURCES), MODEL_LIB_PATH)
+    if verbose:
+        print("built", MODEL_LIB_PATH)
+    return MODEL_LIB_PATH
+
+
 if __name__ == "__main__":
     build(verbose=True)
     build_binding(verbose=True)
+    build_model(verbose=True)
+    build_model_binding(verbose=True)
     sys.exit(0)

@@ -124,6 +124,15 @@ def _outputs(what: str, result):
     return result[1:]
 
 
+def _tensors(values):
+    """The tensors among the values, and in lists and tuples of them."""
+    for v in values:
+        if isinstance(v, torch.Tensor):
+            yield v
+        elif isinstance(v, (list, tuple)):
+            yield from _tensors(v)
+
+
 def _on_stream(stream, what: str, function, t, *args):
     """``function(t, *args)``, a call without a stream of its own, on the stream
     that the caller named: it is current for the call.
@@ -133,8 +142,9 @@ def _on_stream(stream, what: str, function, t, *args):
     call is recorded on the named stream, so that memory of other streams is
     kept until it is done, and the outputs on the caller's, which is to read
     them and may release them before it has."""
-    if isinstance(t, torch.Tensor) and t.is_cuda and stream.device != t.device:
-        raise ValueError("%s: the stream is on %s, the tensors on %s" % (what, stream.device, t.device))
+    first = next(_tensors((t, args)), None)
+    if first is not None and first.is_cuda and stream.device != first.device:
+        raise ValueError("%s: the stream is on %s, the tensors on %s" % (what, stream.device, first.device))
     caller = torch.cuda.current_stream(stream.device)
     with torch.cuda.device(stream.device):  # setting a stream makes its GPU current too
         torch.cuda.set_stream(stream)       # 3 us less than torch.cuda.stream
@@ -143,9 +153,8 @@ def _on_stream(stream, what: str, function, t, *args):
         finally:
             torch.cuda.set_stream(caller)
     outputs = result if isinstance(result, tuple) else (result,)
-    for x in (t, *args, *outputs):
-        if isinstance(x, torch.Tensor):
-            x.record_stream(stream)
+    for x in _tensors((t, args, outputs)):
+        x.record_stream(stream)
     for x in outputs:
         if x is not None:
             x.record_stream(caller)
