@@ -281,7 +281,7 @@ def test_empty_calls_and_given_buffers():
     x, ids, w = tokens_of(5, 2, 4, 64, 3)
     want = layer(x, ids, w)
     out = torch.full((6, 64), 3.0, device=dev, dtype=torch.bfloat16)
-    ws = torch.zeros(fq.fp8q_moe_experts_workspace(5, 2, 32) + 64, dtype=torch.uint8, device=dev)
+    ws = torch.zeros(fq.fp8q_moe_experts_workspace(5, 2, 64, 32) + 64, dtype=torch.uint8, device=dev)
     ws[-64:] = 99
     got = layer(x, ids, w, out=out[:5], workspace=ws[:-64])
     assert got.data_ptr() == out.data_ptr() and torch.equal(out[:5], want)
@@ -290,7 +290,7 @@ def test_empty_calls_and_given_buffers():
     nothing = Layer(BF16, 4, 64, 0, 1)
     assert not nothing(x, ids, w).any()
     assert Layer(BF16, 4, 0, 16, 1)(x[:, :0].contiguous(), ids, w).shape == (5, 0)
-    assert fq.fp8q_moe_experts_workspace(5, 2, 32, torch.float32) == 3 * 2 * 10 * 32
+    assert fq.fp8q_moe_experts_workspace(5, 2, 64, 32, torch.float32) == 3 * 2 * 10 * 32
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
