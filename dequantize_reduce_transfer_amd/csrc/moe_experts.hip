@@ -31,12 +31,27 @@ enum RowFormat : int { kBf16 = 0, kE4M3 = 1, kE5M2 = 2, kMx8 = 3 };   // fp8q_ro
 constexpr uint32_t kMaxPairs = 1024;     // FP8Q_EXPERTS_MAX_PAIRS
 constexpr int kGateUpWaves = 4;          // of a gate_up workgroup: they share the k's
 constexpr int kDownWaves = 8;            // of a down workgroup: they share the experts
-constexpr int kRowsWaves = 4;            // of a down_rows workgroup: 16 rows each
-constexpr uint32_t kFewPairs = 32;       // pairs up to which one kernel multiplies and adds up
+constexpr uint32_t kFewPairs = 24;       // pairs up to which one kernel multiplies and adds up
 
-__device__ __forceinline__ int expert_of(const void *ids, bool ids64, uint32_t p, uint32_t experts) {
-  const int64_t v = ids64 ? static_cast<const int64_t *>(ids)[p] : static_cast<const int *>(ids)[p];
-  return v >= 0 && v < (int64_t)experts ? (int)v : -1;
+// The experts of pairs p[0 .. N), -1 where they have none (an id outside the
+// experts, or a pair that does not exist).  The ids' loads are on their way
+// together: a branch on their type for each would wait for each.
+template <int N>
+__device__ __forceinline__ void experts_of(const void *ids, bool ids64, const uint32_t (&p)[N], uint32_t pairs,
+                                           uint32_t experts, int (&e)[N]) {
+  if (ids64) {
+    int64_t v[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = static_cast<const int64_t *>(ids)[p[i] < pairs ? p[i] : 0u];
+#pragma unroll
+    for (int i = 0; i < N; ++i) e[i] = p[i] < pairs && v[i] >= 0 && v[i] < (int64_t)experts ? (int)v[i] : -1;
+  } else {
+    int v[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = static_cast<const int *>(ids)[p[i] < pairs ? p[i] : 0u];
+#pragma unroll
+    for (int i = 0; i < N; ++i) e[i] = p[i] < pairs && v[i] >= 0 && v[i] < (int)experts ? v[i] : -1;
+  }
 }
 
 // A wave's tile of weights in LDS: R rows of 256 bytes, as 16-byte pieces, which
@@ -58,6 +73,10 @@ __device__ __forceinline__ void lds_done() { asm volatile("s_waitcnt lgkmcnt(0)"
 
 template <int F>
 constexpr uint32_t kPiece = F == kBf16 ? 8 : 16;    // elements of a piece
+template <int F>
+constexpr uint32_t kTile = 16 * kPiece<F>;          // elements of a tile's row
+template <int F>
+constexpr int kVectors = F == kBf16 ? 1 : 2;        // operands of a piece
 
 template <int F>
 __host__ __device__ __forceinline__ uint64_t row_bytes(uint32_t k) {
@@ -68,36 +87,69 @@ __host__ __device__ __forceinline__ uint64_t scale_bytes(uint32_t k) {
   return F == kBf16 ? 0 : F == kMx8 ? k / kMxBlock : 4ull * ((k + kBlock - 1) / kBlock);
 }
 
-// The last bytes [at, at + 16) of a row that ends inside them, zeros behind.
-__device__ __forceinline__ u32x4 load_row_end(const uint8_t *row, uint32_t at, uint32_t bytes) {
-  if (bytes >= 16) return shift_down(load16<false>(row + bytes - 16), at + 16 - bytes, 8);
+// Bytes [at, at + 16) of a row, zeros past its end.
+__device__ __forceinline__ u32x4 load_up_to(const uint8_t *row, uint32_t at, uint32_t bytes) {
+  if (bytes >= 16u) {
+    const uint32_t from = at + 16u <= bytes ? at : bytes - 16u;
+    return shift_down(load16<false>(row + from), at - from, 8);
+  }
   u32x4 v = {0u, 0u, 0u, 0u};
-  for (uint32_t j = 0; at + j < bytes; ++j) v[j / 4] |= (uint32_t)row[at + j] << (8 * (j % 4));
+#pragma unroll 1
+  for (uint32_t j = 0; at + j < bytes; ++j) {
+    const uint32_t byte = (uint32_t)row[at + j] << (8 * (j % 4));
+#pragma unroll
+    for (uint32_t i = 0; i < 4; ++i) v[i] |= j / 4 == i ? byte : 0u;
+  }
   return v;
 }
 
-// Loads the tile of rows [0, R) (those from `rows` on: the last row again) and
-// bytes [at, at + 256) into LDS, all inside the rows; `width` bytes a row.
-//   ALIGNED  rows and their length are multiples of 16 bytes: straight into LDS
-template <int R, bool ALIGNED>
-__device__ __forceinline__ void load_tile(uint8_t *tile, const uint8_t *base, uint32_t rows, uint32_t width,
-                                          uint32_t at, uint32_t lane) {
-  u32x4 v[ALIGNED ? 1 : R / 4];
+// The loads of a tile: rows [0, R) (those from `rows` on: the last row again) and
+// bytes [at, at + 256) of them; `width` bytes a row.
+//   DIRECT  rows and their length are multiples of 16 bytes: straight into LDS;
+//           otherwise through registers, which `commit` writes to LDS, so that
+//           several tiles' loads may be on their way together
+template <int R, bool DIRECT>
+struct TileLoad {
+  u32x4 v[DIRECT ? 1 : R / 4];
+
+  // All of them inside the rows.
+  __device__ __forceinline__ void issue(uint8_t *tile, const uint8_t *base, uint32_t rows, uint32_t width,
+                                        uint32_t at, uint32_t lane) {
 #pragma unroll
-  for (uint32_t i = 0; i < R / 4; ++i) {
-    const uint32_t row = i * 4 + lane / 16u, p = (lane % 16u) ^ row;
-    const uint32_t n = row < rows ? row : rows - 1;
-    const uint8_t *from = base + (uint64_t)n * width + (at + p * 16u);
-    if constexpr (ALIGNED)
-      __builtin_amdgcn_global_load_lds((GlobalPtr)from, (LdsPtr)(tile + i * 1024), 16, 0, 0);
-    else
-      v[i] = load16<false>(from);
+    for (uint32_t i = 0; i < R / 4; ++i) {
+      const uint32_t row = i * 4 + lane / 16u, p = (lane % 16u) ^ row;
+      const uint32_t n = row < rows ? row : rows - 1;
+      const uint8_t *from = base + (uint64_t)n * width + (at + p * 16u);
+      if constexpr (DIRECT)
+        __builtin_amdgcn_global_load_lds((GlobalPtr)from, (LdsPtr)(tile + i * 1024), 16, 0, 2);
+      else
+        v[i] = load16<false>(from);
+    }
   }
-  if constexpr (!ALIGNED) {
+
+  // Rows that end before at + 256: zeros behind (DIRECT: the last piece again,
+  // which the reader replaces).
+  __device__ __forceinline__ void issue_end(uint8_t *tile, const uint8_t *base, uint32_t rows, uint32_t width,
+                                            uint32_t at, uint32_t lane) {
 #pragma unroll
-    for (uint32_t i = 0; i < R / 4; ++i) *reinterpret_cast<u32x4 *>(tile + i * 1024 + lane * 16u) = v[i];
+    for (uint32_t i = 0; i < R / 4; ++i) {
+      const uint32_t row = i * 4 + lane / 16u, b = at + ((lane % 16u) ^ row) * 16u;
+      const uint8_t *from = base + (uint64_t)(row < rows ? row : rows - 1) * width;
+      if constexpr (DIRECT)
+        __builtin_amdgcn_global_load_lds((GlobalPtr)(from + (b < width ? b : width - 16u)), (LdsPtr)(tile + i * 1024),
+                                         16, 0, 2);
+      else
+        v[i] = load_up_to(from, b, width);
+    }
   }
-}
+
+  __device__ __forceinline__ void commit(uint8_t *tile, uint32_t lane) const {
+    if constexpr (!DIRECT) {
+#pragma unroll
+      for (uint32_t i = 0; i < R / 4; ++i) *reinterpret_cast<u32x4 *>(tile + i * 1024 + lane * 16u) = v[i];
+    }
+  }
+};
 
 // The lane's piece of chunk c (four pieces a row).
 template <int R>
@@ -136,7 +188,7 @@ __device__ __forceinline__ float scale_of(uint32_t w) {
   return __uint_as_float(F == kMx8 ? (w & 0xFFu) << 23 : w);
 }
 
-// Scales of a lane's row over four chunks (256 k's): fp32 a block of 128, or
+// Scales of a lane's row over a tile of codes (256 k's): fp32 a block of 128, or
 // E8M0 codes of four blocks of 32 a word.
 template <int F>
 struct Scales {
@@ -148,185 +200,271 @@ struct Scales {
     w[0] = v.x;
     w[1] = v.y;
   }
+
+  // Where the row ends inside the tile: behind its last block anything finite.
+  __device__ __forceinline__ void load_end(const uint8_t *row, uint32_t e, uint32_t k) {
+    if constexpr (F == kMx8) {
+      const uint32_t blocks = k / kMxBlock, at = e / kMxBlock;
+      uint64_t v = 0;
+      if (blocks >= 8) {
+        const u32x2 u = load8<false>(row + blocks - 8);
+        v = (u.x | (uint64_t)u.y << 32) >> (8 * (at + 8 - blocks));
+      } else {
+#pragma unroll 1
+        for (uint32_t i = 0; i < blocks; ++i) v |= (uint64_t)row[i] << (8 * i);
+      }
+      w[0] = (uint32_t)v;
+      w[1] = (uint32_t)(v >> 32);
+    } else if constexpr (F != kBf16) {
+      const uint32_t *p = reinterpret_cast<const uint32_t *>(row);
+      w[0] = p[e / kBlock];
+      w[1] = p[(k - 1) / kBlock];
+    }
+  }
+
   __device__ __forceinline__ float of(int c, uint32_t q) const {
     return scale_of<F>(F == kMx8 ? w[c / 2] >> (16 * (c % 2) + 8 * (q / 2u)) : w[c / 2]);
   }
 };
 
-// What a wave multiplies: N matrices' rows, and the rows of 16 tokens (the
-// lane's one; `parts` elements from one part of a row to the next).
+// A lane's k's of a token's row that one piece of weights meets.
+template <int F, int PARTS>
+struct Operand {
+  u32x4 v[PARTS][kVectors<F>];
+};
+
+// A piece of weights as operands, and its scale.
+template <int F>
+struct Weights {
+  bf16x8 b[kVectors<F>];
+  float scale;
+
+  __device__ __forceinline__ Weights(u32x4 w, float s) : scale(s) {
+    if constexpr (F == kBf16) {
+      b[0] = __builtin_bit_cast(bf16x8, w);
+    } else {
+      b[0] = widen_codes<F>(w.x, w.y, s);
+      b[kVectors<F> - 1] = widen_codes<F>(w.z, w.w, s);
+    }
+  }
+};
+
+// sums += one chunk's products.
+template <int F, int PARTS>
+__device__ __forceinline__ void multiply(f32x4 &sums, const Operand<F, PARTS> &t, const Weights<F> &w) {
+  constexpr bool kScaled = F == kE4M3 || F == kE5M2;
+  f32x4 d = kScaled ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : sums;
+#pragma unroll
+  for (int i = PARTS - 1; i >= 0; --i)                   // the smallest parts first
+#pragma unroll
+    for (int v = 0; v < kVectors<F>; ++v) d = matrix_step(t.v[i][v], w.b[v], d);
+  if constexpr (kScaled) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sums[i] = __builtin_fmaf(w.scale, d[i], sums[i]);
+  } else {
+    sums = d;
+  }
+}
+
+// What a wave multiplies by itself: N matrices' rows, and the rows of 16 tokens
+// (the lane's one; `parts` elements from one part of a row to the next), which
+// it loads straight into registers: few tokens are few lines.
 //   R       rows of a tile
 //   TILES   tiles of each matrix that are loaded at once
 //   PADDED  token rows are zeros from k to the next multiple of 16
-template <int F, int N, int R, int TILES, int PARTS, bool PADDED, bool ALIGNED>
+template <int F, int N, int R, int TILES, int PARTS, bool PADDED, bool DIRECT>
 struct Dot {
-  static constexpr int kVectors = F == kBf16 ? 1 : 2;    // operands of a piece
-  static constexpr uint32_t kTile = 16 * kPiece<F>;      // elements of a tile's row
   static constexpr uint32_t kLds = N * TILES * R * kRowBytes;
   const uint8_t *rows[N];                                // the tile's first row (uniform)
-  const uint8_t *row[N], *scales[N];                     // the lane's
+  const uint8_t *scales[N];                              // the lane's row's
   const uint16_t *token;
   uint64_t parts;
   uint32_t count;                                        // rows there are
   uint32_t k;
   uint8_t *lds;                                          // kLds bytes
 
-  struct Operand {
-    u32x4 v[PARTS][kVectors];
-  };
-
-  // sums += the chunk whose weights are w.
-  __device__ __forceinline__ void multiply(f32x4 &sums, const Operand &t, u32x4 w, float scale) const {
-    constexpr bool kScaled = F == kE4M3 || F == kE5M2;
-    const bf16x8 b0 = F == kBf16 ? __builtin_bit_cast(bf16x8, w) : widen_codes<F>(w.x, w.y, scale);
-    bf16x8 b1 = b0;
-    if constexpr (F != kBf16) b1 = widen_codes<F>(w.z, w.w, scale);
-    f32x4 d = kScaled ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : sums;
-#pragma unroll
-    for (int i = PARTS - 1; i >= 0; --i) {               // the smallest parts first
-      d = matrix_step(t.v[i][0], b0, d);
-      if constexpr (kVectors == 2) d = matrix_step(t.v[i][kVectors - 1], b1, d);
-    }
-    if constexpr (kScaled) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) sums[i] = __builtin_fmaf(scale, d[i], sums[i]);
-    } else {
-      sums = d;
-    }
-  }
-
-  __device__ __forceinline__ void load_tokens(Operand (&t)[4], uint32_t e, uint32_t q) const {
+  __device__ __forceinline__ void load_tokens(Operand<F, PARTS> (&t)[4], uint32_t e, uint32_t q) const {
 #pragma unroll
     for (int c = 0; c < 4; ++c)
 #pragma unroll
       for (int i = 0; i < PARTS; ++i)
 #pragma unroll
-        for (int v = 0; v < kVectors; ++v)
+        for (int v = 0; v < kVectors<F>; ++v)
           t[c].v[i][v] = load16<false>(token + i * parts + e + (c * 4u + q) * kPiece<F> + 8u * v);
   }
 
-  // sums[n] += over W whole tiles' k's from element e on.
-  template <int W>
+  // Zeros past the row's end.
+  __device__ __forceinline__ void load_tokens_end(Operand<F, PARTS> (&t)[4], uint32_t e, uint32_t q) const {
+    const uint32_t end = PADDED ? (k + 15u) / 16u * 16u : k;
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+#pragma unroll
+      for (int i = 0; i < PARTS; ++i)
+#pragma unroll
+        for (int v = 0; v < kVectors<F>; ++v) {
+          const uint32_t at = e + (c * 4u + q) * kPiece<F> + 8u * v;
+          const uint16_t *row = token + i * parts;
+          if constexpr (PADDED || DIRECT) {              // end is a multiple of 8
+            const u32x4 x = load16<false>(row + (at < end ? at : 0u)), zero = {0u, 0u, 0u, 0u};
+            t[c].v[i][v] = at < end ? x : zero;
+          } else {
+            t[c].v[i][v] = load_up_to(reinterpret_cast<const uint8_t *>(row), 2u * at, 2u * end);
+          }
+        }
+  }
+
+  // sums[n] += over W tiles' k's from element e on; END: the row ends in the last.
+  template <int W, bool END>
   __device__ __forceinline__ void stage(f32x4 (&sums)[N], uint32_t e, uint32_t lane) const {
     const uint32_t r = lane % 16u, q = lane / 16u, width = (uint32_t)row_bytes<F>(k);
+    const auto tile = [&](int w, int n) { return lds + (w * N + n) * (R * kRowBytes); };
+    TileLoad<R, DIRECT> loads[W][N];
     Scales<F> s[N][W];
 #pragma unroll
     for (int w = 0; w < W; ++w)
 #pragma unroll
       for (int n = 0; n < N; ++n) {
-        load_tile<R, ALIGNED>(lds + (w * N + n) * (R * kRowBytes), rows[n], count, width,
-                              (uint32_t)row_bytes<F>(e + w * kTile), lane);
-        s[n][w].load(scales[n], e + w * kTile);
+        const uint32_t at = (uint32_t)row_bytes<F>(e + w * kTile<F>);
+        if constexpr (END) {
+          loads[w][n].issue_end(tile(w, n), rows[n], count, width, at, lane);
+          s[n][w].load_end(scales[n], e, k);
+        } else {
+          loads[w][n].issue(tile(w, n), rows[n], count, width, at, lane);
+          s[n][w].load(scales[n], e + w * kTile<F>);
+        }
       }
     // the tokens' rows, two tiles of them in registers
-    Operand t[2][4];
-    load_tokens(t[0], e, q);
-    if constexpr (W > 1) load_tokens(t[1], e + kTile, q);
+    Operand<F, PARTS> t[W > 1 ? 2 : 1][4];
+    if constexpr (END)
+      load_tokens_end(t[0], e, q);
+    else
+      load_tokens(t[0], e, q);
+    if constexpr (W > 1) load_tokens(t[1], e + kTile<F>, q);
     loads_issued();
+#pragma unroll
+    for (int w = 0; w < W; ++w)
+#pragma unroll
+      for (int n = 0; n < N; ++n) loads[w][n].commit(tile(w, n), lane);
     all_loaded();
-    if (!ALIGNED) lds_done();
+    if (!DIRECT) lds_done();
 #pragma unroll
     for (int w = 0; w < W; ++w) {
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
 #pragma unroll
-        for (int n = 0; n < N; ++n)
-          multiply(sums[n], t[w % 2][c], read_piece<R>(lds + (w * N + n) * (R * kRowBytes), c, r, q), s[n][w].of(c, q));
+        for (int n = 0; n < N; ++n) {
+          u32x4 v = read_piece<R>(tile(w, n), c, r, q);
+          if (END && DIRECT && (uint32_t)row_bytes<F>(e) + (c * 4u + q) * 16u >= width) v = u32x4{0u, 0u, 0u, 0u};
+          multiply<F, PARTS>(sums[n], t[W > 1 ? w % 2 : 0][c], Weights<F>(v, s[n][w].of(c, q)));
+        }
         loads_issued();
       }
-      if (w + 2 < W) load_tokens(t[w % 2], e + (w + 2) * kTile, q);
+      if (w + 2 < W) load_tokens(t[w % 2], e + (w + 2) * kTile<F>, q);
     }
     lds_done();                                          // before the next tiles overwrite these
   }
 
-  // sums[n] += over the k's from element e on, fewer than a tile's.
-  __device__ __forceinline__ void tail(f32x4 (&sums)[N], uint32_t e, uint32_t lane) const {
-    const uint32_t q = lane / 16u, width = (uint32_t)row_bytes<F>(k);
-#pragma unroll 1
-    for (; e < k; e += 4 * kPiece<F>) {
-      const uint32_t kk = e + q * kPiece<F>, b = (uint32_t)row_bytes<F>(kk);
-      const u32x4 zero = {0u, 0u, 0u, 0u};
-      Operand t;
+  // sums += over tiles [t0, t1).
+  __device__ __forceinline__ void run(f32x4 (&sums)[N], uint32_t t0, uint32_t t1, uint32_t lane) const {
+    const uint32_t whole = k / kTile<F> < t1 ? k / kTile<F> : t1;
+    uint32_t i = t0;
+    for (; i + TILES <= whole; i += TILES) stage<TILES, false>(sums, i * kTile<F>, lane);
+    if constexpr (TILES > 1)
+      for (; i < whole; ++i) stage<1, false>(sums, i * kTile<F>, lane);
+    if (whole < t1 && t0 < t1 && whole * kTile<F> < k) stage<1, true>(sums, whole * kTile<F>, lane);
+  }
+};
+
+// Tiles of a row's k's, the last one partial.
+template <int F>
+__host__ __device__ __forceinline__ uint32_t tiles_of(uint32_t k) {
+  return (k + kTile<F> - 1) / kTile<F>;
+}
+
+struct Layer {
+  const uint16_t *x;
+  const void *ids;
+  const float *weights;
+  bool ids64, out_bf16;
+  bool by_pair;                          // a workgroup's expert is a pair's
+  uint32_t tokens, topk, pairs, experts, hidden, inter;
+  uint32_t padded;                       // inter, up to a multiple of 16
+  uint32_t groups;                       // workgroups an expert
+  ExpertMatrix gate, up, down;
+  uint16_t *h;                           // [parts][pairs][padded]: 2 or 3 bf16 numbers an h
+  float *y;                              // [pairs][hidden]
+  void *out;
+};
+
+// The pairs of a workgroup's expert: expert `which`, or (by_pair) the one of pair
+// `which` if no pair before it has the same.
+struct Pairs {
+  int e;
+  uint32_t count;                        // 0 where there is nothing to do
+
+  // Every wave scans all pairs; wave 0 writes those of rank [m0, m0 + most) to
+  // `list`, which a barrier has to follow.
+  __device__ __forceinline__ Pairs(const Layer &a, uint32_t which, uint32_t m0, uint32_t most, uint16_t *list) {
+    constexpr uint32_t kAtOnce = 4;      // loads of 64 ids on their way together
+    const uint32_t lane = lane_id(), wid = uniform(threadIdx.x / kWave);
+    e = (int)which;
+    count = 0;
+    for (uint32_t p0 = 0; p0 < a.pairs; p0 += kAtOnce * kWave) {
+      uint32_t p[kAtOnce + 1];
+      int id[kAtOnce + 1];
 #pragma unroll
-      for (int i = 0; i < PARTS; ++i)
+      for (uint32_t i = 0; i < kAtOnce; ++i) p[i] = p0 + i * kWave + lane;
+      p[kAtOnce] = which;
+      experts_of(a.ids, a.ids64, p, a.pairs, a.experts, id);
+      if (a.by_pair) e = (int)uniform((uint32_t)id[kAtOnce]);
 #pragma unroll
-        for (int v = 0; v < kVectors; ++v) {
-          const uint16_t *p = token + i * parts;
-          const uint32_t at = kk + 8u * v, end = PADDED ? (k + 15u) / 16u * 16u : k;
-          t.v[i][v] = at + 8u <= end ? load16<false>(p + at)
-                      : at < end     ? load_row_end(reinterpret_cast<const uint8_t *>(p), 2u * at, 2u * end)
-                                     : zero;
+      for (uint32_t i = 0; i < kAtOnce; ++i) {
+        const bool same = id[i] == e && e >= 0;
+        const uint64_t mask = __builtin_amdgcn_ballot_w64(same);
+        if (a.by_pair && count == 0 && mask && p0 + i * kWave + (uint32_t)__builtin_ctzll(mask) != which) {
+          e = -1;                        // another workgroup's
+          return;
         }
-#pragma unroll
-      for (int n = 0; n < N; ++n) {
-        const u32x4 w = b + 16u <= width ? load16<false>(row[n] + b) : b < width ? load_row_end(row[n], b, width) : zero;
-        uint32_t s = 0;
-        if constexpr (F == kMx8)
-          s = kk < k ? scales[n][kk / kMxBlock] : 127u;
-        else if constexpr (F != kBf16)
-          s = reinterpret_cast<const uint32_t *>(scales[n])[e / kBlock];
-        multiply(sums[n], t, w, scale_of<F>(s));
+        const uint32_t rank = count + __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32),
+                                                                __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0));
+        if (same && wid == 0 && rank - m0 < most) list[rank - m0] = (uint16_t)p[i];
+        count += (uint32_t)__builtin_popcountll(mask);
       }
     }
   }
-
-  // Tiles of a row's k's, the last one partial.
-  static __host__ __device__ __forceinline__ uint32_t tiles(uint32_t k) { return (k + kTile - 1) / kTile; }
-
-  // sums += over tiles [t0, t1).
-  __device__ __forceinline__ void run(f32x4 (&sums)[N], uint32_t t0, uint32_t t1, uint32_t lane) const {
-    const uint32_t whole = k / kTile < t1 ? k / kTile : t1;
-    uint32_t i = t0;
-    for (; i + TILES <= whole; i += TILES) stage<TILES>(sums, i * kTile, lane);
-    if constexpr (TILES > 1)
-      for (; i < whole; ++i) stage<1>(sums, i * kTile, lane);
-    if (whole < t1 && t0 < t1) tail(sums, whole * kTile, lane);
-  }
 };
 
-// The pairs of the workgroup's expert (number `which`, or by_pair the one of
-// pair `which` if no pair before it has the same) into `list`, by wave 0; how
-// many there are, 0 where there is nothing to do.
-__device__ __forceinline__ uint32_t expert_pairs(const void *ids, bool ids64, bool by_pair, uint32_t pairs,
-                                                 uint32_t experts, uint32_t which, uint16_t *list, int &e) {
-  const uint32_t lane = lane_id(), wid = uniform(threadIdx.x / kWave);
-  e = (int)which;
-  if (by_pair) {
-    e = expert_of(ids, ids64, which, experts);
-    if (e < 0) return 0;
+// silu(g) * u.
+__device__ __forceinline__ float gated(float g, float u) { return g / (1.0f + expf(-g)) * u; }
+
+// h of a pair at a column of its padded row (zeros from inter on), as a sum of
+// bf16 numbers: its leading bits, and the rest's.  Two hold 16 of its bits, which
+// is far past what a bf16 output shows; three hold them all.  (An inf or NaN has
+// no rest.)
+__device__ __forceinline__ void store_h(const Layer &a, uint32_t pair, uint32_t column, float h) {
+  if (column >= a.padded) return;
+  if (column >= a.inter) h = 0.0f;
+  uint16_t *to = a.h + (uint64_t)pair * a.padded + column;
+  const uint64_t part = (uint64_t)a.pairs * a.padded;
+  const uint32_t bits = __float_as_uint(h);
+  to[0] = (uint16_t)(h != h ? 0x7FC0u : bits >> 16);
+  const bool finite = (bits & 0x7F800000u) != 0x7F800000u;
+  const float rest = finite ? h - __uint_as_float(bits & 0xFFFF0000u) : 0.0f;
+  if (a.out_bf16) {
+    to[part] = (uint16_t)round2_bf16(rest, 0.0f);
+  } else {
+    const uint32_t b = __float_as_uint(rest);
+    to[part] = (uint16_t)(b >> 16);
+    to[2 * part] = (uint16_t)round2_bf16(rest - __uint_as_float(b & 0xFFFF0000u), 0.0f);
   }
-  uint32_t count = 0;
-  for (uint32_t p0 = 0; p0 < pairs; p0 += kWave) {
-    const uint32_t p = p0 + lane;
-    const bool same = p < pairs && expert_of(ids, ids64, p, experts) == e;
-    const uint64_t mask = __builtin_amdgcn_ballot_w64(same);
-    if (by_pair && count == 0 && mask && p0 + (uint32_t)__builtin_ctzll(mask) != which) return 0;
-    if (same && wid == 0)
-      list[count + __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0))] =
-          (uint16_t)p;
-    count += (uint32_t)__builtin_popcountll(mask);
-  }
-  __syncthreads();
-  return count;
 }
-
-struct GateUp {
-  const uint16_t *x;
-  const void *ids;
-  bool ids64, by_pair;
-  uint32_t pairs, topk, experts, hidden, inter, tiles;
-  uint32_t padded;                       // inter, up to a multiple of 16
-  int parts;                             // bf16 numbers that make an h: 2 or 3
-  ExpertMatrix gate, up;
-  uint16_t *h;                           // [parts][pairs][padded]
-};
 
 template <int F, bool ALIGNED>
 using GateUpDot = Dot<F, 2, 16, 1, 1, false, ALIGNED>;
 
 // h of up to 16 pairs of one expert, for 16 of its rows.
 template <int F, bool ALIGNED>
-__device__ __forceinline__ void gate_up_tile(const GateUp &a, uint32_t e, uint32_t n0, const uint16_t *list,
+__device__ __forceinline__ void gate_up_tile(const Layer &a, uint32_t e, uint32_t n0, const uint16_t *list,
                                              uint32_t count, uint8_t *lds) {
   const uint32_t lane = lane_id(), r = lane % 16u, q = lane / 16u, wid = uniform(threadIdx.x / kWave);
   const uint32_t n = n0 + r < a.inter ? n0 + r : a.inter - 1;
@@ -340,10 +478,8 @@ __device__ __forceinline__ void gate_up_tile(const GateUp &a, uint32_t e, uint32
   dot.scales[0] = a.gate.scales + (a.gate.expert_rows * e + n) * scale_bytes<F>(a.hidden);
   dot.scales[1] = a.up.scales + (a.up.expert_rows * e + n) * scale_bytes<F>(a.hidden);
   dot.token = a.x + (uint64_t)(list[r < count ? r : count - 1] / a.topk) * a.hidden;
-  dot.row[0] = dot.rows[0] + (n - n0) * row_bytes<F>(a.hidden);
-  dot.row[1] = dot.rows[1] + (n - n0) * row_bytes<F>(a.hidden);
   f32x4 sums[2] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
-  const uint32_t tiles = dot.tiles(a.hidden);
+  const uint32_t tiles = tiles_of<F>(a.hidden);
   dot.run(sums, tiles * wid / kGateUpWaves, tiles * (wid + 1) / kGateUpWaves, lane);
   __syncthreads();                       // the tiles' memory is the sums' now
   float *sums_lds = reinterpret_cast<float *>(lds);
@@ -363,50 +499,23 @@ __device__ __forceinline__ void gate_up_tile(const GateUp &a, uint32_t e, uint32
       g += sums_lds[w * 512u + at];
       u += sums_lds[w * 512u + 256u + at];
     }
-    float h = g / (1.0f + expf(-g)) * u;
-    if (col >= a.inter) h = 0.0f;        // the padding
-    // h as a sum of bf16 numbers: its leading bits, and the rest's.  (An inf
-    // or NaN has no rest.)
-    uint16_t *to = a.h + (uint64_t)list[c] * a.padded + col;
-    const uint64_t part = (uint64_t)a.pairs * a.padded;
-    const uint32_t bits = __float_as_uint(h);
-    const bool finite = (bits & 0x7F800000u) != 0x7F800000u;
-    to[0] = (uint16_t)(h != h ? 0x7FC0u : bits >> 16);
-    const float rest = finite ? h - __uint_as_float(bits & 0xFFFF0000u) : 0.0f;
-    if (a.parts == 2) {
-      to[part] = (uint16_t)round2_bf16(rest, 0.0f);
-    } else {
-      const uint32_t b = __float_as_uint(rest);
-      to[part] = (uint16_t)(b >> 16);
-      to[2 * part] = (uint16_t)round2_bf16(rest - __uint_as_float(b & 0xFFFF0000u), 0.0f);
-    }
+    store_h(a, list[c], col, gated(g, u));
   }
 }
 
 template <int F, bool ALIGNED>
-__global__ __launch_bounds__(64 * kGateUpWaves) void gate_up_kernel(const GateUp a) {
-  __shared__ uint16_t list[kMaxPairs];
+__global__ __launch_bounds__(64 * kGateUpWaves) void gate_up_kernel(const Layer a) {
+  __shared__ uint16_t list[kFewPairs];
   __shared__ alignas(16) uint8_t lds[kGateUpWaves * GateUpDot<F, ALIGNED>::kLds];
-  const uint32_t n0 = blockIdx.x % a.tiles * 16u;
-  int e;
-  const uint32_t count = expert_pairs(a.ids, a.ids64, a.by_pair, a.pairs, a.experts, blockIdx.x / a.tiles, list, e);
-  if (count == 0) return;
-  for (uint32_t m0 = 0; m0 < count; m0 += 16u) {
+  const uint32_t n0 = blockIdx.x % a.groups * 16u;
+  const Pairs pairs(a, blockIdx.x / a.groups, 0, kFewPairs, list);
+  if (pairs.count == 0) return;
+  __syncthreads();
+  for (uint32_t m0 = 0; m0 < pairs.count; m0 += 16u) {
     if (m0) __syncthreads();
-    gate_up_tile<F, ALIGNED>(a, (uint32_t)e, n0, list + m0, count - m0 < 16u ? count - m0 : 16u, lds);
+    gate_up_tile<F, ALIGNED>(a, (uint32_t)pairs.e, n0, list + m0, pairs.count - m0 < 16u ? pairs.count - m0 : 16u, lds);
   }
 }
-
-struct Down {
-  const uint16_t *h;
-  const void *ids;
-  const float *weights;
-  bool ids64, by_pair, out_bf16;
-  uint32_t tokens, topk, experts, hidden, inter, padded, groups;
-  ExpertMatrix down;
-  float *y;                              // [pairs][hidden], of down_rows_kernel
-  void *out;
-};
 
 template <int F, int R, int TILES, int PARTS, bool ALIGNED>
 using DownDot = Dot<F, 1, R, TILES, PARTS, true, ALIGNED>;
@@ -414,25 +523,24 @@ using DownDot = Dot<F, 1, R, TILES, PARTS, true, ALIGNED>;
 // The product of up to 16 pairs of one expert with R of its rows, over tiles
 // [t0, t1) of the k's.
 template <int F, int R, int TILES, int PARTS, bool ALIGNED>
-__device__ __forceinline__ f32x4 down_tile(const Down &a, uint32_t e, uint32_t n0, uint32_t pair, uint32_t t0,
+__device__ __forceinline__ f32x4 down_tile(const Layer &a, uint32_t e, uint32_t n0, uint32_t pair, uint32_t t0,
                                            uint32_t t1, uint8_t *lds) {
   const uint32_t lane = lane_id(), r = lane % 16u;
   const uint32_t n = n0 + r % R < a.hidden ? n0 + r % R : a.hidden - 1;
   DownDot<F, R, TILES, PARTS, ALIGNED> dot;
   dot.k = a.inter;
-  dot.parts = (uint64_t)a.tokens * a.topk * a.padded;
+  dot.parts = (uint64_t)a.pairs * a.padded;
   dot.count = a.hidden - n0;
   dot.lds = lds;
   dot.rows[0] = a.down.rows + (a.down.expert_rows * e + n0) * row_bytes<F>(a.inter);
   dot.scales[0] = a.down.scales + (a.down.expert_rows * e + n) * scale_bytes<F>(a.inter);
   dot.token = a.h + (uint64_t)pair * a.padded;
-  dot.row[0] = dot.rows[0] + (n - n0) * row_bytes<F>(a.inter);
   f32x4 sums[1] = {{0.0f, 0.0f, 0.0f, 0.0f}};
   dot.run(sums, t0, t1, lane);
   return sums[0];
 }
 
-__device__ __forceinline__ void store_out(const Down &a, uint64_t at, float v) {
+__device__ __forceinline__ void store_out(const Layer &a, uint64_t at, float v) {
   if (a.out_bf16)
     static_cast<uint16_t *>(a.out)[at] = (uint16_t)round2_bf16(v, 0.0f);
   else
@@ -442,14 +550,18 @@ __device__ __forceinline__ void store_out(const Down &a, uint64_t at, float v) {
 // Up to 64 pairs: a workgroup takes R rows of every expert that a pair names,
 // the waves an expert (or a part of its k's) each, and adds the pairs up.
 template <int F, int R, int PARTS, bool ALIGNED>
-__global__ __launch_bounds__(64 * kDownWaves) void down_kernel(const Down a) {
-  constexpr int kTiles = 3;
+__global__ __launch_bounds__(64 * kDownWaves) void down_kernel(const Layer a) {
+  constexpr int kTiles = PARTS == 3 ? 1 : 3;       // what the registers hold
   __shared__ float y[kDownWaves * kFewPairs * R];  // [split][pair][row]
+  __shared__ float weights[kFewPairs];
   __shared__ alignas(16) uint8_t tiles[kDownWaves * DownDot<F, R, kTiles, PARTS, ALIGNED>::kLds];
   const uint32_t tid = threadIdx.x, lane = lane_id(), wid = uniform(tid / kWave);
-  const uint32_t pairs = a.tokens * a.topk, n0 = blockIdx.x * (uint32_t)R, r = lane % 16u, q = lane / 16u;
+  const uint32_t pairs = a.pairs, n0 = blockIdx.x * (uint32_t)R, r = lane % 16u, q = lane / 16u;
   // lane p's pair: the others of its expert, and whether it is their first
-  const int e = lane < pairs ? expert_of(a.ids, a.ids64, lane, a.experts) : -1;
+  if (tid < pairs) weights[tid] = a.weights[tid];
+  int es[1];
+  experts_of(a.ids, a.ids64, {lane}, pairs, a.experts, es);
+  const int e = es[0];
   uint64_t same = __builtin_amdgcn_ballot_w64(e >= 0);
   const uint64_t held = same;
   for (uint32_t b = 1; b < a.experts; b <<= 1) {
@@ -460,7 +572,7 @@ __global__ __launch_bounds__(64 * kDownWaves) void down_kernel(const Down a) {
   uint64_t first = __builtin_amdgcn_ballot_w64(e >= 0 && (uint32_t)__builtin_ctzll(same) == lane);
   // where experts are fewer than waves, several waves share one's k's
   const uint32_t experts = (uint32_t)__builtin_popcountll(first);
-  const uint32_t whole = DownDot<F, R, kTiles, PARTS, ALIGNED>::tiles(a.inter);
+  const uint32_t whole = tiles_of<F>(a.inter);
   uint32_t splits = 1;
   while (experts * splits * 2 <= (uint32_t)kDownWaves && splits * 2 <= whole) splits *= 2;
   for (uint32_t item = 0; item < experts * splits; ++item) {
@@ -495,46 +607,225 @@ __global__ __launch_bounds__(64 * kDownWaves) void down_kernel(const Down a) {
       if (!(held >> p & 1)) continue;
       float v = 0.0f;
       for (uint32_t s = 0; s < splits; ++s) v += y[(s * pairs + p) * R + c];
-      sum = __builtin_fmaf(a.weights[p], v, sum);
+      sum = __builtin_fmaf(weights[p], v, sum);
     }
     store_out(a, (uint64_t)t * a.hidden + n0 + c, sum);
   }
 }
 
-// y of the pairs of one expert, 16 rows a wave.
-template <int F, int PARTS, bool ALIGNED>
-__global__ __launch_bounds__(64 * kRowsWaves) void down_rows_kernel(const Down a) {
-  constexpr int kTiles = 3;
-  __shared__ uint16_t list[kMaxPairs];
-  __shared__ alignas(16) uint8_t tiles[kRowsWaves * DownDot<F, 16, kTiles, PARTS, ALIGNED>::kLds];
-  const uint32_t lane = lane_id(), wid = uniform(threadIdx.x / kWave), r = lane % 16u, q = lane / 16u;
-  int e;
-  const uint32_t count = expert_pairs(a.ids, a.ids64, a.by_pair, a.tokens * a.topk, a.experts, blockIdx.x / a.groups,
-                                      list, e);
-  const uint32_t n0 = (blockIdx.x % a.groups * kRowsWaves + wid) * 16u;
-  if (count == 0 || n0 >= a.hidden) return;
-  for (uint32_t m0 = 0; m0 < count; m0 += 16u) {
-    const uint32_t n = count - m0 < 16u ? count - m0 : 16u;
-    const f32x4 sums = down_tile<F, 16, kTiles, PARTS, ALIGNED>(
-        a, (uint32_t)e, n0, list[m0 + (r < n ? r : n - 1)], 0, ~0u, tiles + wid * DownDot<F, 16, kTiles, PARTS, ALIGNED>::kLds);
+// out_t = sum of the token's y: lane j has the token's j-th expert and weight.
+__global__ __launch_bounds__(256) void combine_kernel(const Layer a) {
+  const uint32_t column = blockIdx.x * 256u + threadIdx.x, p0 = blockIdx.y * a.topk, lane = lane_id();
+  const float weight = a.weights[p0 + (lane < a.topk ? lane : 0u)];
+  int e[1];
+  experts_of(a.ids, a.ids64, {p0 + lane}, lane < a.topk ? a.pairs : 0u, a.experts, e);
+  uint64_t held = __builtin_amdgcn_ballot_w64(e[0] >= 0);
+  const float *y = a.y + (uint64_t)p0 * a.hidden + (column < a.hidden ? column : 0u);
+  float sum = 0.0f;
+  constexpr int kAtOnce = 8;             // loads on their way together
+  while (held) {
+    float v[kAtOnce], w[kAtOnce];
 #pragma unroll
-    for (uint32_t i = 0; i < 4; ++i)
-      if (4u * q + i < n && n0 + r < a.hidden) a.y[(uint64_t)list[m0 + 4u * q + i] * a.hidden + n0 + r] = sums[i];
+    for (int i = 0; i < kAtOnce; ++i) {
+      const uint32_t j = held ? (uint32_t)__builtin_ctzll(held) : 0u;
+      w[i] = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(weight), (int)j));
+      v[i] = held ? y[(uint64_t)j * a.hidden] : 0.0f;
+      if (!held) w[i] = 0.0f;
+      held &= held - 1;
+    }
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) sum = __builtin_fmaf(w[i], v[i], sum);
   }
+  if (column < a.hidden) store_out(a, (uint64_t)blockIdx.y * a.hidden + column, sum);
 }
 
-// out_t = sum of the token's y.
-__global__ __launch_bounds__(256) void combine_kernel(const Down a) {
-  const uint32_t column = blockIdx.x * 256u + threadIdx.x, t = blockIdx.y;
-  if (column >= a.hidden) return;
-  float sum = 0.0f;
-#pragma unroll 4
-  for (uint32_t j = 0; j < a.topk; ++j) {
-    const uint32_t p = t * a.topk + j;
-    if (expert_of(a.ids, a.ids64, p, a.experts) < 0) continue;
-    sum = __builtin_fmaf(a.weights[p], a.y[(uint64_t)p * a.hidden + column], sum);
+// Many tokens an expert: the workgroup's waves take 16 rows each of gate and of
+// up (or twice 16 of down), and share the tokens' rows, which go through LDS as
+// the weights do: straight from memory into registers, 16 tokens are 16 rows a
+// load.
+constexpr int kWideWaves = 4;
+
+template <int F, int M, int PARTS>
+constexpr uint32_t kTokenBytes = PARTS * M * 16 * 2 * kTile<F>;
+
+// sums[n][m] = products of the wave's rows (rows[n]: the first one's, scales[n]:
+// the lane's one's) with 16 M tokens' rows.
+template <int F, int M, int PARTS, bool PADDED, bool DIRECT>
+struct WideDot {
+  const uint8_t *rows[2], *scales[2];
+  uint32_t count[2];                                     // rows there are
+  uint32_t k;
+  const uint8_t *tokens;
+  uint8_t *weights_lds;                                  // the wave's: 2 tiles
+  uint8_t *tokens_lds;                                   // kTokenBytes
+
+  // A token's 256 or 512 bytes of a tile are pieces of 16; a load takes whole
+  // rows of them, and piece p of token c lies in place p ^ (c % 16).
+  static constexpr uint32_t kPieces = 2 * kTile<F> / 16;
+  static constexpr uint32_t kUnits = kTokenBytes<F, M, PARTS> / 1024;
+  static constexpr uint32_t kLoads = (kUnits + kWideWaves - 1) / kWideWaves;   // a wave's
+  uint32_t from[kLoads];                                 // the lane's rows' bytes into `tokens`, one a load
+
+  // list: the pairs (all 16 M); a pair's row is pair / per * stride bytes into
+  // `tokens`, its parts part_bytes apart.
+  __device__ __forceinline__ void find(const uint16_t *list, uint32_t count, uint32_t per, uint32_t stride,
+                                       uint32_t part_bytes, uint32_t lane, uint32_t wid) {
+#pragma unroll
+    for (uint32_t i = 0; i < kLoads; ++i) {
+      const uint32_t row = ((wid * kLoads + i) * 64u + lane) / kPieces, c = row % (16u * M);
+      from[i] = list[c < count ? c : count - 1] / per * stride + row / (16u * M) * part_bytes;
+    }
   }
-  store_out(a, (uint64_t)t * a.hidden + column, sum);
+
+  template <bool END>
+  __device__ __forceinline__ void stage(f32x4 (&sums)[2][M], uint32_t e, uint32_t lane, uint32_t wid) const {
+    const uint32_t r = lane % 16u, q = lane / 16u, width = (uint32_t)row_bytes<F>(k), at = (uint32_t)row_bytes<F>(e);
+    TileLoad<16, DIRECT> loads[2];
+    Scales<F> s[2];
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+      if constexpr (END) {
+        loads[n].issue_end(weights_lds + n * 4096, rows[n], count[n], width, at, lane);
+        s[n].load_end(scales[n], e, k);
+      } else {
+        loads[n].issue(weights_lds + n * 4096, rows[n], count[n], width, at, lane);
+        s[n].load(scales[n], e);
+      }
+    }
+    constexpr bool kTokensDirect = PADDED || DIRECT;     // rows are multiples of 16 bytes
+    const uint32_t end = 2u * (PADDED ? (k + 15u) / 16u * 16u : k);
+    u32x4 v[kTokensDirect ? 1 : kLoads];
+#pragma unroll
+    for (uint32_t i = 0; i < kLoads; ++i) {
+      if (kUnits % kWideWaves && wid * kLoads + i >= kUnits) break;
+      const uint32_t unit = (wid * kLoads + i) * 64u + lane, row = unit / kPieces, c = row % (16u * M);
+      const uint32_t p = (unit % kPieces) ^ (c % 16u), b = 2u * e + p * 16u;
+      const uint8_t *row_at = tokens + from[i];
+      if constexpr (kTokensDirect)
+        __builtin_amdgcn_global_load_lds((GlobalPtr)(row_at + (!END || b < end ? b : 0u)),
+                                         (LdsPtr)(tokens_lds + (wid * kLoads + i) * 1024u), 16, 0, 0);
+      else
+        v[i] = END ? load_up_to(row_at, b, end) : load16<false>(row_at + b);
+    }
+    loads_issued();
+#pragma unroll
+    for (int n = 0; n < 2; ++n) loads[n].commit(weights_lds + n * 4096, lane);
+    if constexpr (!kTokensDirect) {
+#pragma unroll
+      for (uint32_t i = 0; i < kLoads; ++i)
+        if (kUnits % kWideWaves == 0 || wid * kLoads + i < kUnits)
+          *reinterpret_cast<u32x4 *>(tokens_lds + (wid * kLoads + i) * 1024u + lane * 16u) = v[i];
+    }
+    all_loaded();
+    __syncthreads();
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      u32x4 x[2];
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        x[n] = read_piece<16>(weights_lds + n * 4096, c, r, q);
+        if (END && DIRECT && at + (c * 4u + q) * 16u >= width) x[n] = u32x4{0u, 0u, 0u, 0u};
+      }
+      const Weights<F> w[2] = {{x[0], s[0].of(c, q)}, {x[1], s[1].of(c, q)}};
+#pragma unroll
+      for (int m = 0; m < M; ++m) {
+        Operand<F, PARTS> t;
+#pragma unroll
+        for (int i = 0; i < PARTS; ++i)
+#pragma unroll
+          for (int j = 0; j < kVectors<F>; ++j) {
+            const uint32_t p = (c * 4u + q) * kVectors<F> + j;
+            u32x4 v = *reinterpret_cast<const u32x4 *>(
+                tokens_lds + ((i * M + m) * 16u + r) * (kPieces * 16u) + ((p ^ r) * 16u));
+            if (END && kTokensDirect && 2u * e + p * 16u >= end) v = u32x4{0u, 0u, 0u, 0u};
+            t.v[i][j] = v;
+          }
+#pragma unroll
+        for (int n = 0; n < 2; ++n) multiply<F, PARTS>(sums[n][m], t, w[n]);
+        if (m % 2 || m + 1 == M) loads_issued();
+      }
+    }
+    __syncthreads();                                     // before the next stage's loads overwrite these
+  }
+
+  __device__ __forceinline__ void run(f32x4 (&sums)[2][M], uint32_t lane, uint32_t wid) const {
+    uint32_t e = 0;
+    for (; e + kTile<F> <= k; e += kTile<F>) stage<false>(sums, e, lane, wid);
+    if (e < k) stage<true>(sums, e, lane, wid);
+  }
+};
+
+// h of `count` pairs of one expert, up to 16 M, for the workgroup's 64 rows of
+// gate and up from n0 on, or their y for its 128 rows of down.  `list`, which
+// holds them, is in tokens_lds.
+template <int F, bool DOWN, int M, int PARTS, bool DIRECT>
+__device__ __forceinline__ void wide_tile(const Layer &a, uint32_t e, uint32_t n0, uint16_t *list, uint32_t count,
+                                          uint8_t *weights_lds, uint8_t *tokens_lds) {
+  const uint32_t lane = lane_id(), r = lane % 16u, q = lane / 16u, wid = uniform(threadIdx.x / kWave);
+  const uint32_t rows = DOWN ? a.hidden : a.inter, k = DOWN ? a.inter : a.hidden;
+  WideDot<F, M, PARTS, DOWN, DIRECT> dot;
+  dot.k = k;
+  uint32_t first[2];
+#pragma unroll
+  for (int n = 0; n < 2; ++n) {
+    const ExpertMatrix &w = DOWN ? a.down : n ? a.up : a.gate;
+    first[n] = n0 + (DOWN ? (wid * 2u + n) * 16u : wid * 16u);
+    // a wave past the last row takes that one
+    const uint32_t from = first[n] < rows ? first[n] : rows - 1, row = from + r < rows ? from + r : rows - 1;
+    dot.count[n] = rows - from;
+    dot.rows[n] = w.rows + (w.expert_rows * e + from) * row_bytes<F>(k);
+    dot.scales[n] = w.scales + (w.expert_rows * e + row) * scale_bytes<F>(k);
+  }
+  dot.tokens = reinterpret_cast<const uint8_t *>(DOWN ? a.h : a.x);
+  dot.find(list, count, DOWN ? 1u : a.topk, 2u * (DOWN ? a.padded : a.hidden), a.pairs * a.padded * 2u, lane, wid);
+  dot.weights_lds = weights_lds + wid * 8192u;
+  dot.tokens_lds = tokens_lds;
+  // a thread's pair, kept while the list's memory is the tokens'
+  const uint16_t mine = list[threadIdx.x < count ? threadIdx.x : 0u];
+  __syncthreads();
+  f32x4 sums[2][M];
+#pragma unroll
+  for (int m = 0; m < M; ++m) sums[0][m] = sums[1][m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  dot.run(sums, lane, wid);
+  if (threadIdx.x < 16 * M) list[threadIdx.x] = mine;
+  __syncthreads();
+#pragma unroll
+  for (int m = 0; m < M; ++m)
+#pragma unroll
+    for (uint32_t i = 0; i < 4; ++i) {
+      const uint32_t c = 16u * m + 4u * q + i;
+      if (c >= count) continue;
+      const uint32_t p = list[c];
+      if constexpr (DOWN) {
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+          if (first[n] + r < rows) a.y[(uint64_t)p * a.hidden + first[n] + r] = sums[n][m][i];
+      } else {
+        store_h(a, p, first[0] + r, gated(sums[0][m][i], sums[1][m][i]));
+      }
+    }
+}
+
+template <int F, bool DOWN, int M, int PARTS, bool DIRECT>
+__global__ __launch_bounds__(64 * kWideWaves) void wide_kernel(const Layer a) {
+  __shared__ alignas(16) uint8_t weights[kWideWaves * 8192];
+  __shared__ alignas(16) uint8_t tokens[kTokenBytes<F, M, PARTS>];
+  uint16_t *list = reinterpret_cast<uint16_t *>(tokens);
+  const uint32_t n0 = blockIdx.x % a.groups * (kWideWaves * (DOWN ? 32u : 16u));
+  for (uint32_t m0 = 0;; m0 += 16u * M) {
+    const Pairs pairs(a, blockIdx.x / a.groups, m0, 16u * M, list);
+    if (pairs.count <= m0) return;
+    const uint32_t left = pairs.count - m0, e = (uint32_t)pairs.e;
+    __syncthreads();
+    if (M > 1 && left <= 16u)
+      wide_tile<F, DOWN, 1, PARTS, DIRECT>(a, e, n0, list, left, weights, tokens);
+    else if (M > 2 && left <= 32u)
+      wide_tile<F, DOWN, 2, PARTS, DIRECT>(a, e, n0, list, left, weights, tokens);
+    else
+      wide_tile<F, DOWN, M, PARTS, DIRECT>(a, e, n0, list, left < 16u * M ? left : 16u * M, weights, tokens);
+    if (left <= 16u * M) return;
+    __syncthreads();
+  }
 }
 
 uint32_t padded(uint32_t inter) { return (inter + 15u) / 16u * 16u; }
@@ -544,64 +835,72 @@ bool aligned_rows(const ExpertMatrix &m, uint32_t k) {
   return reinterpret_cast<uintptr_t>(m.rows) % 16 == 0 && row_bytes<F>(k) % 16 == 0;
 }
 
-template <int F, bool ALIGNED>
-void gate_up_launch(const GateUp &g, hipStream_t stream) {
-  hipLaunchKernelGGL((gate_up_kernel<F, ALIGNED>), dim3((g.by_pair ? g.pairs : g.experts) * g.tiles),
-                     dim3(64 * kGateUpWaves), 0, stream, g);
-}
-
-template <int F, int R, bool ALIGNED>
-void down_launch(const Down &d, hipStream_t stream) {
-  const dim3 grid((d.hidden + R - 1) / R), block(64 * kDownWaves);
-  if (d.out_bf16)
-    hipLaunchKernelGGL((down_kernel<F, R, 2, ALIGNED>), grid, block, 0, stream, d);
-  else
-    hipLaunchKernelGGL((down_kernel<F, R, 3, ALIGNED>), grid, block, 0, stream, d);
-}
-
-template <int F, bool ALIGNED>
-void down_rows_launch(const Down &d, hipStream_t stream) {
-  const dim3 grid((d.by_pair ? d.tokens * d.topk : d.experts) * d.groups), block(64 * kRowsWaves);
-  if (d.out_bf16)
-    hipLaunchKernelGGL((down_rows_kernel<F, 2, ALIGNED>), grid, block, 0, stream, d);
-  else
-    hipLaunchKernelGGL((down_rows_kernel<F, 3, ALIGNED>), grid, block, 0, stream, d);
-}
-
 // Bytes of the workspace's h, a multiple of 16.
 uint64_t h_bytes(uint32_t pairs, uint32_t inter, bool out_bf16) {
   return 2ull * (out_bf16 ? 2 : 3) * pairs * padded(inter);
 }
 
-template <int F>
-hipError_t experts_launch(const MoeExperts &a, hipStream_t stream) {
-  const uint32_t pairs = a.tokens * a.topk;
-  if (a.inter) {
-    const GateUp g{a.x, a.ids, a.ids64, pairs < a.experts, pairs, a.topk, a.experts, a.hidden, a.inter,
-                   (a.inter + 15u) / 16u, padded(a.inter), a.out_bf16 ? 2 : 3, a.gate, a.up, a.workspace};
-    if (aligned_rows<F>(a.gate, a.hidden) && aligned_rows<F>(a.up, a.hidden))
-      gate_up_launch<F, true>(g, stream);
+// A launch of `groups` workgroups an expert.
+template <typename Kernel>
+hipError_t by_expert(Kernel kernel, Layer a, uint32_t groups, uint32_t waves, hipStream_t stream) {
+  a.groups = groups;
+  hipLaunchKernelGGL(kernel, dim3((a.by_pair ? a.pairs : a.experts) * groups), dim3(64 * waves), 0, stream, a);
+  return hipGetLastError();
+}
+
+// The wide kernel for `m` x 16 tokens an expert.
+template <int F, bool DOWN, int PARTS, bool DIRECT>
+hipError_t wide_launch(const Layer &a, int m, hipStream_t stream) {
+  const uint32_t groups = DOWN ? (a.hidden + 127u) / 128u : (a.inter + 63u) / 64u;
+  return m == 1   ? by_expert(wide_kernel<F, DOWN, 1, PARTS, DIRECT>, a, groups, kWideWaves, stream)
+         : m == 2 ? by_expert(wide_kernel<F, DOWN, 2, PARTS, DIRECT>, a, groups, kWideWaves, stream)
+                  : by_expert(wide_kernel<F, DOWN, 4, PARTS, DIRECT>, a, groups, kWideWaves, stream);
+}
+
+template <int F, bool DIRECT>
+hipError_t gate_up(const Layer &a, int wide, hipStream_t stream) {
+  if (wide) return wide_launch<F, false, 1, DIRECT>(a, wide, stream);
+  return by_expert(gate_up_kernel<F, DIRECT>, a, (a.inter + 15u) / 16u, kGateUpWaves, stream);
+}
+
+template <int F, int PARTS, bool DIRECT>
+hipError_t down(const Layer &a, int wide, hipStream_t stream) {
+  if (!wide) {
+    const dim3 block(64 * kDownWaves);
+    if (a.hidden < 4096)
+      hipLaunchKernelGGL((down_kernel<F, 8, PARTS, DIRECT>), dim3((a.hidden + 7u) / 8u), block, 0, stream, a);
     else
-      gate_up_launch<F, false>(g, stream);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-  }
-  const Down d{a.workspace, a.ids, a.weights, a.ids64, pairs < a.experts, a.out_bf16, a.tokens, a.topk,
-               a.inter ? a.experts : 0, a.hidden, a.inter, padded(a.inter), (a.hidden + 16 * kRowsWaves - 1) / (16 * kRowsWaves),
-               a.down, reinterpret_cast<float *>(a.workspace + h_bytes(pairs, a.inter, a.out_bf16) / 2), a.out};
-  const bool aligned = aligned_rows<F>(a.down, a.inter);
-  if (pairs <= kFewPairs || a.inter == 0) {
-    if (aligned)
-      d.hidden < 4096 ? down_launch<F, 8, true>(d, stream) : down_launch<F, 16, true>(d, stream);
-    else
-      d.hidden < 4096 ? down_launch<F, 8, false>(d, stream) : down_launch<F, 16, false>(d, stream);
+      hipLaunchKernelGGL((down_kernel<F, 16, PARTS, DIRECT>), dim3((a.hidden + 15u) / 16u), block, 0, stream, a);
     return hipGetLastError();
   }
-  aligned ? down_rows_launch<F, true>(d, stream) : down_rows_launch<F, false>(d, stream);
-  const hipError_t e = hipGetLastError();
+  const hipError_t e = wide_launch<F, true, PARTS, DIRECT>(a, wide, stream);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(combine_kernel, dim3((a.hidden + 255u) / 256u, a.tokens), dim3(256), 0, stream, d);
+  hipLaunchKernelGGL(combine_kernel, dim3((a.hidden + 255u) / 256u, a.tokens), dim3(256), 0, stream, a);
   return hipGetLastError();
+}
+
+// 0: few pairs; else how many times 16 tokens the wide kernels hold.
+int wide_of(uint32_t pairs, uint32_t experts) {
+  if (pairs <= kFewPairs) return 0;
+  const uint32_t each = (pairs + experts - 1) / experts;
+  return each <= 10 ? 1 : each <= 20 ? 2 : 4;
+}
+
+template <int F>
+hipError_t experts_launch(const MoeExperts &m, hipStream_t stream) {
+  const uint32_t pairs = m.tokens * m.topk;
+  const Layer a{m.x, m.ids, m.weights, m.ids64, m.out_bf16, pairs < m.experts, m.tokens, m.topk, pairs,
+                m.inter ? m.experts : 0, m.hidden, m.inter, padded(m.inter), 0, m.gate, m.up, m.down, m.workspace,
+                reinterpret_cast<float *>(m.workspace + h_bytes(pairs, m.inter, m.out_bf16) / 2), m.out};
+  const int wide = m.inter ? wide_of(pairs, m.experts) : 0;
+  if (m.inter) {
+    const bool direct = aligned_rows<F>(m.gate, m.hidden) && aligned_rows<F>(m.up, m.hidden);
+    const hipError_t e = direct ? gate_up<F, true>(a, wide, stream) : gate_up<F, false>(a, wide, stream);
+    if (e != hipSuccess) return e;
+  }
+  const bool direct = aligned_rows<F>(m.down, m.inter);
+  if (m.out_bf16) return direct ? down<F, 2, true>(a, wide, stream) : down<F, 2, false>(a, wide, stream);
+  return direct ? down<F, 3, true>(a, wide, stream) : down<F, 3, false>(a, wide, stream);
 }
 
 }  // namespace
