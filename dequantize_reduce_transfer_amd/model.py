@@ -177,7 +177,7 @@ def fp8q_grad_sumsq(grads: Sequence[torch.Tensor], scales: Optional[Sequence] = 
     128 codes, or one.  Summed in fp64, in an order that the sizes fix.  Its
     square root is the global norm; over ranks that hold different gradients
     the sums add up (``all_reduce``) before :func:`fp8q_grad_clip`.
-    ``workspace``: uint8; 16 KiB for every 112 gradients begun are always enough.
+    ``workspace``: uint8; 16 KiB for every 160 gradients begun are always enough.
     """
     if stream is not None:
         return _on_stream(stream, "fp8q_grad_sumsq", fp8q_grad_sumsq, grads, scales, fmt, out, workspace)

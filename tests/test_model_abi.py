@@ -197,11 +197,14 @@ def test_grad_validation():
     assert L().fp8q_grad_sumsq(g, 4, None, P(ws.addr), 1 << 16, None) == ERR_NULL
     assert L().fp8q_grad_sumsq(g, 4, P(total.addr + 4), P(ws.addr), 1 << 16, None) == ERR_ALIGN
     assert L().fp8q_grad_sumsq(g, 4, P(total.addr), P(ws.addr + 8), 1 << 15, None) == ERR_ALIGN
-    assert L().fp8q_grad_sumsq(g, 4, P(total.addr), P(ws.addr), 7, None) == ERR_ARG
-    assert L().fp8q_grad_sumsq(g, 4, P(total.addr), None, 1 << 16, None) == ERR_NULL
-    for at in (a.addr + 8, b.addr, q.addr, s.addr + 8, one.addr, ws.addr):
-        assert L().fp8q_grad_sumsq(g, 4, P(at // 8 * 8), P(ws.addr), 1 << 16, None) == ERR_OVERLAP
-    assert L().fp8q_grad_sumsq(g, 4, P(total.addr), P(a.addr), 1 << 16, None) == ERR_OVERLAP
+    many = Buf(1 << 20)                      # a list that needs a workspace
+    large = grads((many, None, 1 << 18, 0, 0), *good)
+    assert L().fp8q_grad_sumsq(large, 5, P(total.addr), P(ws.addr), 7, None) == ERR_ARG
+    assert L().fp8q_grad_sumsq(large, 5, P(total.addr), None, 1 << 16, None) == ERR_NULL
+    for at in (a.addr + 8, b.addr, q.addr, s.addr + 8, one.addr, many.addr + 4096, ws.addr):
+        assert L().fp8q_grad_sumsq(large, 5, P(at // 8 * 8), P(ws.addr), 1 << 16, None) == ERR_OVERLAP
+    for at in (a.addr, many.addr + 4096):
+        assert L().fp8q_grad_sumsq(large, 5, P(total.addr), P(at), 1 << 16, None) == ERR_OVERLAP
     for bad in (dict(m=-1.0), dict(m=float("nan")), dict(e=-1.0), dict(e=float("nan")), dict(e=float("inf"))):
         assert L().fp8q_grad_clip(g, 4, P(total.addr), bad.get("m", 1.0), bad.get("e", 1e-6), P(norm.addr),
                                   None) == ERR_ARG, bad
