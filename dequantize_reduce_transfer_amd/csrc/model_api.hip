@@ -62,8 +62,8 @@ Extent extent_of(const fp8q_expert_matrix &m, fp8q_row_format format, int expert
   return {{m.rows, count * width * (format == FP8Q_ROWS_BF16 ? 2 : 1)}, {m.scales, scales}};
 }
 
-bool experts_sizes_ok(size_t tokens, int topk, size_t hidden, size_t inter, fp8q_out_dtype out_dtype) {
-  return topk >= 1 && topk <= FP8Q_MAX_TOPK && tokens <= FP8Q_EXPERTS_MAX_PAIRS / (size_t)topk &&
+bool experts_sizes_ok(size_t tokens, int topk, int experts, size_t hidden, size_t inter, fp8q_out_dtype out_dtype) {
+  return experts >= 1 && experts <= FP8Q_MAX_EXPERTS && topk >= 1 && topk <= FP8Q_MAX_TOPK && tokens <= FP8Q_EXPERTS_MAX_PAIRS / (size_t)topk &&
          hidden <= FP8Q_EXPERTS_MAX_SIZE && inter <= FP8Q_EXPERTS_MAX_SIZE &&
          (out_dtype == FP8Q_OUT_F32 || out_dtype == FP8Q_OUT_BF16);
 }
@@ -145,9 +145,11 @@ fp8q_status fp8q_moe_route_backward(const float *dweights, const void *logits, f
   return from_hip(fp8q::launch_moe_route_backward(a, static_cast<hipStream_t>(stream)));
 }
 
-size_t fp8q_moe_experts_workspace(size_t tokens, int topk, size_t hidden, size_t inter, fp8q_out_dtype out_dtype) {
-  if (!experts_sizes_ok(tokens, topk, hidden, inter, out_dtype)) return 0;
-  return (size_t)fp8q::moe_experts_workspace((uint32_t)(tokens * topk), (uint32_t)hidden, (uint32_t)inter,
+size_t fp8q_moe_experts_workspace(size_t tokens, int topk, int experts, size_t hidden, size_t inter,
+                                  fp8q_out_dtype out_dtype) {
+  if (!experts_sizes_ok(tokens, topk, experts, hidden, inter, out_dtype) || tokens == 0) return 0;
+  return (size_t)fp8q::moe_experts_workspace((uint32_t)(tokens * topk), (uint32_t)experts, (uint32_t)hidden,
+                                             (uint32_t)inter,
                                              out_dtype == FP8Q_OUT_BF16);
 }
 
@@ -159,11 +161,10 @@ fp8q_status fp8q_moe_experts(const void *x_bf16, const void *ids, int id_bytes, 
   if (format != FP8Q_ROWS_BF16 && format != FP8Q_ROWS_E4M3 && format != FP8Q_ROWS_E5M2 && format != FP8Q_ROWS_MX8)
     return FP8Q_ERR_ARG;
   if (id_bytes != 4 && id_bytes != 8) return FP8Q_ERR_ARG;
-  if (!experts_sizes_ok(tokens, topk, hidden, inter, out_dtype) || experts < 1 || experts > FP8Q_MAX_EXPERTS)
-    return FP8Q_ERR_ARG;
+  if (!experts_sizes_ok(tokens, topk, experts, hidden, inter, out_dtype)) return FP8Q_ERR_ARG;
   if (format == FP8Q_ROWS_MX8 && (hidden % FP8Q_MX_BLOCK || inter % FP8Q_MX_BLOCK)) return FP8Q_ERR_ARG;
   if (tokens == 0 || hidden == 0) return FP8Q_OK;
-  const uint64_t need = fp8q_moe_experts_workspace(tokens, topk, hidden, inter, out_dtype);
+  const uint64_t need = fp8q_moe_experts_workspace(tokens, topk, experts, hidden, inter, out_dtype);
   if (workspace_bytes < need) return FP8Q_ERR_ARG;
   if (!gate || !up || !down || !x_bf16 || !ids || !weights || !out || (need && !workspace)) return FP8Q_ERR_NULL;
   if (!aligned(x_bf16, 16) || !aligned(out, 16) || !aligned(workspace, 16) || !aligned(ids, (uintptr_t)id_bytes) ||

@@ -137,7 +137,7 @@ PyObject *moe_experts(PyObject *, PyObject *const *args, Py_ssize_t n) {
     const bool bf16 = c.truth(10, "out_dtype");
     const fp8q_out_dtype dtype = bf16 ? FP8Q_OUT_BF16 : FP8Q_OUT_F32;
     const at::Tensor out = c.output(11, "out", bf16 ? at::kBFloat16 : at::kFloat, {tokens, hidden});
-    const at::Tensor ws = c.workspace(12, fp8q_moe_experts_workspace(tokens, (int)ids.size(1), hidden, inter, dtype));
+    const at::Tensor ws = c.workspace(12, fp8q_moe_experts_workspace(tokens, (int)ids.size(1), (int)experts, hidden, inter, dtype));
     const c10::DeviceGuard on(c.device());
     const fp8q_status st = fp8q_moe_experts(
         ptr(x), ptr(ids), (int)ids.element_size(), f32(weights), gate.format, &gate.m, &up.m, &down.m, tokens,

@@ -68,7 +68,7 @@ struct MoeExperts {
   bool out_bf16;
   uint16_t *workspace;        // moe_experts_workspace bytes
 };
-uint64_t moe_experts_workspace(uint32_t pairs, uint32_t hidden, uint32_t inter, bool out_bf16);
+uint64_t moe_experts_workspace(uint32_t pairs, uint32_t experts, uint32_t hidden, uint32_t inter, bool out_bf16);
 // format: the fp8q_row_format values.
 hipError_t launch_moe_experts(int format, const MoeExperts &a, hipStream_t stream);
 

@@ -390,9 +390,10 @@ struct Layer {
   uint32_t tokens, topk, pairs, experts, hidden, inter;
   uint32_t padded;                       // inter, up to a multiple of 16
   uint32_t groups;                       // workgroups an expert
+  uint32_t splits;                       // parts of down's k's, a workgroup and a y each
   ExpertMatrix gate, up, down;
   uint16_t *h;                           // [parts][pairs][padded]: 2 or 3 bf16 numbers an h
-  float *y;                              // [pairs][hidden]
+  float *y;                              // [splits][pairs][hidden]
   void *out;
 };
 
@@ -621,6 +622,7 @@ __global__ __launch_bounds__(256) void combine_kernel(const Layer a) {
   experts_of(a.ids, a.ids64, {p0 + lane}, lane < a.topk ? a.pairs : 0u, a.experts, e);
   uint64_t held = __builtin_amdgcn_ballot_w64(e[0] >= 0);
   const float *y = a.y + (uint64_t)p0 * a.hidden + (column < a.hidden ? column : 0u);
+  const uint64_t split = (uint64_t)a.pairs * a.hidden;
   float sum = 0.0f;
   constexpr int kAtOnce = 8;             // loads on their way together
   while (held) {
@@ -631,6 +633,7 @@ __global__ __launch_bounds__(256) void combine_kernel(const Layer a) {
       w[i] = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(weight), (int)j));
       v[i] = held ? y[(uint64_t)j * a.hidden] : 0.0f;
       if (!held) w[i] = 0.0f;
+      for (uint32_t s = 1; s < a.splits; ++s) v[i] += held ? y[s * split + (uint64_t)j * a.hidden] : 0.0f;
       held &= held - 1;
     }
 #pragma unroll
@@ -748,10 +751,14 @@ struct WideDot {
     __syncthreads();                                     // before the next stage's loads overwrite these
   }
 
-  __device__ __forceinline__ void run(f32x4 (&sums)[2][M], uint32_t lane, uint32_t wid) const {
-    uint32_t e = 0;
-    for (; e + kTile<F> <= k; e += kTile<F>) stage<false>(sums, e, lane, wid);
-    if (e < k) stage<true>(sums, e, lane, wid);
+  // over tiles [t0, t1) of the rows
+  __device__ __forceinline__ void run(f32x4 (&sums)[2][M], uint32_t t0, uint32_t t1, uint32_t lane, uint32_t wid) const {
+    for (uint32_t t = t0; t < t1; ++t) {
+      if ((t + 1) * kTile<F> <= k)
+        stage<false>(sums, t * kTile<F>, lane, wid);
+      else
+        stage<true>(sums, t * kTile<F>, lane, wid);
+    }
   }
 };
 
@@ -759,7 +766,7 @@ struct WideDot {
 // gate and up from n0 on, or their y for its 128 rows of down.  `list`, which
 // holds them, is in tokens_lds.
 template <int F, bool DOWN, int M, int PARTS, bool DIRECT>
-__device__ __forceinline__ void wide_tile(const Layer &a, uint32_t e, uint32_t n0, uint16_t *list, uint32_t count,
+__device__ __forceinline__ void wide_tile(const Layer &a, uint32_t e, uint32_t n0, uint32_t split, uint16_t *list, uint32_t count,
                                           uint8_t *weights_lds, uint8_t *tokens_lds) {
   const uint32_t lane = lane_id(), r = lane % 16u, q = lane / 16u, wid = uniform(threadIdx.x / kWave);
   const uint32_t rows = DOWN ? a.hidden : a.inter, k = DOWN ? a.inter : a.hidden;
@@ -786,7 +793,8 @@ __device__ __forceinline__ void wide_tile(const Layer &a, uint32_t e, uint32_t n
   f32x4 sums[2][M];
 #pragma unroll
   for (int m = 0; m < M; ++m) sums[0][m] = sums[1][m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  dot.run(sums, lane, wid);
+  const uint32_t tiles = tiles_of<F>(k), splits = DOWN ? a.splits : 1u;
+  dot.run(sums, tiles * split / splits, tiles * (split + 1) / splits, lane, wid);
   if (threadIdx.x < 16 * M) list[threadIdx.x] = mine;
   __syncthreads();
 #pragma unroll
@@ -799,7 +807,7 @@ __device__ __forceinline__ void wide_tile(const Layer &a, uint32_t e, uint32_t n
       if constexpr (DOWN) {
 #pragma unroll
         for (int n = 0; n < 2; ++n)
-          if (first[n] + r < rows) a.y[(uint64_t)p * a.hidden + first[n] + r] = sums[n][m][i];
+          if (first[n] + r < rows) a.y[((uint64_t)split * a.pairs + p) * a.hidden + first[n] + r] = sums[n][m][i];
       } else {
         store_h(a, p, first[0] + r, gated(sums[0][m][i], sums[1][m][i]));
       }
@@ -811,18 +819,20 @@ __global__ __launch_bounds__(64 * kWideWaves) void wide_kernel(const Layer a) {
   __shared__ alignas(16) uint8_t weights[kWideWaves * 8192];
   __shared__ alignas(16) uint8_t tokens[kTokenBytes<F, M, PARTS>];
   uint16_t *list = reinterpret_cast<uint16_t *>(tokens);
-  const uint32_t n0 = blockIdx.x % a.groups * (kWideWaves * (DOWN ? 32u : 16u));
+  // of a split's workgroups, those of one expert follow one another
+  const uint32_t splits = DOWN ? a.splits : 1u, group = blockIdx.x % (a.groups * splits);
+  const uint32_t n0 = group % a.groups * (kWideWaves * (DOWN ? 32u : 16u)), split = group / a.groups;
   for (uint32_t m0 = 0;; m0 += 16u * M) {
-    const Pairs pairs(a, blockIdx.x / a.groups, m0, 16u * M, list);
+    const Pairs pairs(a, blockIdx.x / (a.groups * splits), m0, 16u * M, list);
     if (pairs.count <= m0) return;
     const uint32_t left = pairs.count - m0, e = (uint32_t)pairs.e;
     __syncthreads();
     if (M > 1 && left <= 16u)
-      wide_tile<F, DOWN, 1, PARTS, DIRECT>(a, e, n0, list, left, weights, tokens);
+      wide_tile<F, DOWN, 1, PARTS, DIRECT>(a, e, n0, split, list, left, weights, tokens);
     else if (M > 2 && left <= 32u)
-      wide_tile<F, DOWN, 2, PARTS, DIRECT>(a, e, n0, list, left, weights, tokens);
+      wide_tile<F, DOWN, 2, PARTS, DIRECT>(a, e, n0, split, list, left, weights, tokens);
     else
-      wide_tile<F, DOWN, M, PARTS, DIRECT>(a, e, n0, list, left < 16u * M ? left : 16u * M, weights, tokens);
+      wide_tile<F, DOWN, M, PARTS, DIRECT>(a, e, n0, split, list, left < 16u * M ? left : 16u * M, weights, tokens);
     if (left <= 16u * M) return;
     __syncthreads();
   }
@@ -835,16 +845,26 @@ bool aligned_rows(const ExpertMatrix &m, uint32_t k) {
   return reinterpret_cast<uintptr_t>(m.rows) % 16 == 0 && row_bytes<F>(k) % 16 == 0;
 }
 
+// Parts of down's k's.  Where the experts' rows alone would not give every CU
+// four workgroups, parts of 1024 k's or more do (256 workgroups of 14336 k's,
+// 128 tokens: one part 246 us, four 1SPLIT us).
+uint32_t splits_of(uint32_t pairs, uint32_t experts, uint32_t hidden, uint32_t inter) {
+  const uint32_t workgroups = (pairs < experts ? pairs : experts) * ((hidden + 127u) / 128u);
+  const uint32_t want = 1024u / workgroups, most = inter / 1024u;
+  const uint32_t n = want < most ? want : most;
+  return n < 1 ? 1 : n < 8 ? n : 8;
+}
+
 // Bytes of the workspace's h, a multiple of 16.
 uint64_t h_bytes(uint32_t pairs, uint32_t inter, bool out_bf16) {
   return 2ull * (out_bf16 ? 2 : 3) * pairs * padded(inter);
 }
 
-// A launch of `groups` workgroups an expert.
+// A launch of `groups` workgroups an expert and split.
 template <typename Kernel>
-hipError_t by_expert(Kernel kernel, Layer a, uint32_t groups, uint32_t waves, hipStream_t stream) {
+hipError_t by_expert(Kernel kernel, Layer a, uint32_t groups, uint32_t splits, uint32_t waves, hipStream_t stream) {
   a.groups = groups;
-  hipLaunchKernelGGL(kernel, dim3((a.by_pair ? a.pairs : a.experts) * groups), dim3(64 * waves), 0, stream, a);
+  hipLaunchKernelGGL(kernel, dim3((a.by_pair ? a.pairs : a.experts) * groups * splits), dim3(64 * waves), 0, stream, a);
   return hipGetLastError();
 }
 
@@ -852,15 +872,16 @@ hipError_t by_expert(Kernel kernel, Layer a, uint32_t groups, uint32_t waves, hi
 template <int F, bool DOWN, int PARTS, bool DIRECT>
 hipError_t wide_launch(const Layer &a, int m, hipStream_t stream) {
   const uint32_t groups = DOWN ? (a.hidden + 127u) / 128u : (a.inter + 63u) / 64u;
-  return m == 1   ? by_expert(wide_kernel<F, DOWN, 1, PARTS, DIRECT>, a, groups, kWideWaves, stream)
-         : m == 2 ? by_expert(wide_kernel<F, DOWN, 2, PARTS, DIRECT>, a, groups, kWideWaves, stream)
-                  : by_expert(wide_kernel<F, DOWN, 4, PARTS, DIRECT>, a, groups, kWideWaves, stream);
+  const uint32_t splits = DOWN ? a.splits : 1u;
+  return m == 1   ? by_expert(wide_kernel<F, DOWN, 1, PARTS, DIRECT>, a, groups, splits, kWideWaves, stream)
+         : m == 2 ? by_expert(wide_kernel<F, DOWN, 2, PARTS, DIRECT>, a, groups, splits, kWideWaves, stream)
+                  : by_expert(wide_kernel<F, DOWN, 4, PARTS, DIRECT>, a, groups, splits, kWideWaves, stream);
 }
 
 template <int F, bool DIRECT>
 hipError_t gate_up(const Layer &a, int wide, hipStream_t stream) {
   if (wide) return wide_launch<F, false, 1, DIRECT>(a, wide, stream);
-  return by_expert(gate_up_kernel<F, DIRECT>, a, (a.inter + 15u) / 16u, kGateUpWaves, stream);
+  return by_expert(gate_up_kernel<F, DIRECT>, a, (a.inter + 15u) / 16u, 1, kGateUpWaves, stream);
 }
 
 template <int F, int PARTS, bool DIRECT>
@@ -890,7 +911,7 @@ template <int F>
 hipError_t experts_launch(const MoeExperts &m, hipStream_t stream) {
   const uint32_t pairs = m.tokens * m.topk;
   const Layer a{m.x, m.ids, m.weights, m.ids64, m.out_bf16, pairs < m.experts, m.tokens, m.topk, pairs,
-                m.inter ? m.experts : 0, m.hidden, m.inter, padded(m.inter), 0, m.gate, m.up, m.down, m.workspace,
+                m.inter ? m.experts : 0, m.hidden, m.inter, padded(m.inter), 0, splits_of(pairs, m.experts, m.hidden, m.inter), m.gate, m.up, m.down, m.workspace,
                 reinterpret_cast<float *>(m.workspace + h_bytes(pairs, m.inter, m.out_bf16) / 2), m.out};
   const int wide = m.inter ? wide_of(pairs, m.experts) : 0;
   if (m.inter) {
@@ -905,9 +926,10 @@ hipError_t experts_launch(const MoeExperts &m, hipStream_t stream) {
 
 }  // namespace
 
-uint64_t moe_experts_workspace(uint32_t pairs, uint32_t hidden, uint32_t inter, bool out_bf16) {
-  if (!inter) return 0;
-  return h_bytes(pairs, inter, out_bf16) + (pairs <= kFewPairs ? 0 : 4ull * pairs * hidden);
+uint64_t moe_experts_workspace(uint32_t pairs, uint32_t experts, uint32_t hidden, uint32_t inter, bool out_bf16) {
+  if (!inter || !hidden) return 0;
+  return h_bytes(pairs, inter, out_bf16) +
+         (pairs <= kFewPairs ? 0 : 4ull * splits_of(pairs, experts, hidden, inter) * pairs * hidden);
 }
 
 hipError_t launch_moe_experts(int format, const MoeExperts &a, hipStream_t stream) {

@@ -67,7 +67,7 @@ def model_lib(path: str = LIB_PATH) -> ctypes.CDLL:
     M, G = ctypes.POINTER(ExpertMatrix), ctypes.POINTER(Grad)
     L.fp8q_moe_route.argtypes = [P, I, S, I, I, I, P, P, P]
     L.fp8q_moe_route_backward.argtypes = [P, P, I, P, P, S, I, I, I, P, P]
-    L.fp8q_moe_experts_workspace.argtypes = [S, I, S, S, I]
+    L.fp8q_moe_experts_workspace.argtypes = [S, I, I, S, S, I]
     L.fp8q_moe_experts.argtypes = [P, P, I, P, I, M, M, M, S, I, I, S, S, P, I, P, S, P]
     L.fp8q_grad_sumsq_workspace.argtypes = [G, S]
     L.fp8q_grad_sumsq.argtypes = [G, S, P, P, S, P]
@@ -157,9 +157,10 @@ def fp8q_moe_experts(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, 
         _out_code(out_dtype) == OUT_BF16, out, workspace, _current(x)))[0]
 
 
-def fp8q_moe_experts_workspace(tokens: int, topk: int, hidden: int, inter: int, out_dtype=torch.bfloat16) -> int:
+def fp8q_moe_experts_workspace(tokens: int, topk: int, experts: int, hidden: int, inter: int,
+                               out_dtype=torch.bfloat16) -> int:
     """Bytes of workspace that :func:`fp8q_moe_experts` needs."""
-    return int(model_lib().fp8q_moe_experts_workspace(tokens, topk, hidden, inter, _out_code(out_dtype)))
+    return int(model_lib().fp8q_moe_experts_workspace(tokens, topk, experts, hidden, inter, _out_code(out_dtype)))
 
 
 def _first(grads, other):

@@ -116,8 +116,8 @@ typedef struct {
  * topk 1 .. FP8Q_MAX_TOPK, experts 1 .. FP8Q_MAX_EXPERTS, tokens * topk up to
  * FP8Q_EXPERTS_MAX_PAIRS, hidden and inter up to FP8Q_EXPERTS_MAX_SIZE.
  */
-FP8Q_API size_t fp8q_moe_experts_workspace(size_t tokens, int topk, size_t hidden, size_t inter,
-                                           fp8q_out_dtype out_dtype);
+FP8Q_API size_t fp8q_moe_experts_workspace(size_t tokens, int topk, int experts, size_t hidden,
+                                           size_t inter, fp8q_out_dtype out_dtype);
 FP8Q_API fp8q_status fp8q_moe_experts(const void *x_bf16, const void *ids, int id_bytes,
                                       const float *weights, fp8q_row_format format,
                                       const fp8q_expert_matrix *gate, const fp8q_expert_matrix *up,

@@ -59,7 +59,7 @@ hipError_t launch_moe_route_backward(const MoeRouteBackward &a, hipStream_t) {
   return ok ? record("moe_route_backward", a.tokens, a.experts) : hipErrorInvalidValue;
 }
 
-uint64_t moe_experts_workspace(uint32_t pairs, uint32_t, uint32_t inter, bool out_bf16) {
+uint64_t moe_experts_workspace(uint32_t pairs, uint32_t, uint32_t, uint32_t inter, bool out_bf16) {
   return (out_bf16 ? 4ull : 6ull) * pairs * inter;
 }
 

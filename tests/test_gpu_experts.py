@@ -131,6 +131,17 @@ def test_counts(fmt, tokens, topk, experts):
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("tokens", [20, 100])
+def test_long_rows_of_few_experts(fmt, tokens):
+    """down's k's in several parts, the last of them ragged (MXFP8: by 32)."""
+    layer = Layer(fmt, 2, 160, 2144 if fmt == MX8 else 2153, 8)
+    x, ids, w = tokens_of(tokens, 2, 2, 160, tokens, gone=0.1)
+    for dtype in (torch.bfloat16, torch.float32):
+        got = check(layer, x, ids, w, dtype)
+        assert torch.equal(layer(x, ids, w, out_dtype=dtype), got)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
 def test_exact_sums(fmt):
     """Small integers throughout, and gates above 32 (there exp(-g) is lost
     beside 1, and silu(g) is g): nothing is rounded, and the fp32 output is the
@@ -281,7 +292,7 @@ def test_empty_calls_and_given_buffers():
     x, ids, w = tokens_of(5, 2, 4, 64, 3)
     want = layer(x, ids, w)
     out = torch.full((6, 64), 3.0, device=dev, dtype=torch.bfloat16)
-    ws = torch.zeros(fq.fp8q_moe_experts_workspace(5, 2, 64, 32) + 64, dtype=torch.uint8, device=dev)
+    ws = torch.zeros(fq.fp8q_moe_experts_workspace(5, 2, 4, 64, 32) + 64, dtype=torch.uint8, device=dev)
     ws[-64:] = 99
     got = layer(x, ids, w, out=out[:5], workspace=ws[:-64])
     assert got.data_ptr() == out.data_ptr() and torch.equal(out[:5], want)
@@ -290,7 +301,7 @@ def test_empty_calls_and_given_buffers():
     nothing = Layer(BF16, 4, 64, 0, 1)
     assert not nothing(x, ids, w).any()
     assert Layer(BF16, 4, 0, 16, 1)(x[:, :0].contiguous(), ids, w).shape == (5, 0)
-    assert fq.fp8q_moe_experts_workspace(5, 2, 64, 32, torch.float32) == 3 * 2 * 10 * 32
+    assert fq.fp8q_moe_experts_workspace(5, 2, 4, 64, 32, torch.float32) == 3 * 2 * 10 * 32
 
 
 @pytest.mark.parametrize("fmt", FORMATS)

@@ -229,13 +229,15 @@ def test_workspaces():
         many = grads(*[(Buf(16), None, 2, 0, 0)] * 300)
         assert 0 < L().fp8q_grad_sumsq_workspace(many, 300) <= 16384 * 3
         # h, its rows filled up to 16; and of many pairs their y
-        assert L().fp8q_moe_experts_workspace(3, 2, 100, 17, 1) == 2 * 2 * 6 * 32
-        assert L().fp8q_moe_experts_workspace(3, 2, 100, 17, 0) == 3 * 2 * 6 * 32
-        assert L().fp8q_moe_experts_workspace(300, 2, 100, 17, 0) == 3 * 2 * 600 * 32 + 4 * 600 * 100
+        assert L().fp8q_moe_experts_workspace(3, 2, 8, 100, 17, 1) == 2 * 2 * 6 * 32
+        assert L().fp8q_moe_experts_workspace(3, 2, 8, 100, 17, 0) == 3 * 2 * 6 * 32
+        assert L().fp8q_moe_experts_workspace(300, 2, 8, 100, 17, 0) == 3 * 2 * 600 * 32 + 4 * 600 * 100
+        # few workgroups of long rows: several parts
+        assert L().fp8q_moe_experts_workspace(300, 2, 8, 1024, 4096, 1) == 2 * 2 * 600 * 4096 + 4 * 4 * 600 * 1024
     assert L().fp8q_grad_sumsq_workspace(grads((None, None, 5, 0, 0)), 1) == 0
-    assert L().fp8q_moe_experts_workspace(1025, 1, 64, 64, 0) == 0
-    assert L().fp8q_moe_experts_workspace(4, 0, 64, 64, 0) == 0
-    assert L().fp8q_moe_experts_workspace(4, 1, 64, 64, 7) == 0
+    assert L().fp8q_moe_experts_workspace(1025, 1, 8, 64, 64, 0) == 0
+    assert L().fp8q_moe_experts_workspace(4, 0, 8, 64, 64, 0) == 0
+    assert L().fp8q_moe_experts_workspace(4, 1, 8, 64, 64, 7) == 0
 
 
 def _stub():
