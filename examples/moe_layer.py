@@ -7,15 +7,17 @@ The layer's path, as a training step takes it on one GPU:
 
   norm      h = x + residual; rms_norm(h) in MXFP8 for the experts and in bf16
             for the router
-  route     softmax of the router's logits, the topk experts of each token
+  route     softmax of the router's logits, the topk experts of each token and
+            their weights
   dispatch  the pairs sorted by expert, and the tokens' 8-bit rows written in
             that order (what an expert-parallel job would send)
   experts   each expert's run of rows through its weight, bf16 (torch matmul)
   combine   the expert rows weighted by the router and summed per token
 
 Backward runs the same path the other way, straight through the 8-bit
-rounding.  The experts' products here stand in for whatever computes them; the
-rest is the library.
+rounding, and the gradients are clipped to a global norm before the update.  The
+experts' products here stand in for whatever computes them; the rest is the
+library.
 """
 from __future__ import annotations
 
@@ -48,6 +50,21 @@ class Norm(torch.autograd.Function):
         h, weight, rstd = ctx.saved_tensors
         dx, dw = fq.fp8q_rms_norm_backward(dy.contiguous(), h, weight, rstd, dh=dh.contiguous())
         return dx, dx, dw.to(weight.dtype), None
+
+
+class Route(torch.autograd.Function):
+    """(weights, ids) of each token's topk experts; the choice has no gradient."""
+
+    @staticmethod
+    def forward(ctx, logits, topk):
+        weights, ids = fq.fp8q_moe_route(logits, topk, normalize=False)
+        ctx.save_for_backward(logits, weights, ids)
+        ctx.mark_non_differentiable(ids)
+        return weights, ids
+
+    @staticmethod
+    def backward(ctx, dweights, _ids):
+        return fq.fp8q_moe_route_backward(dweights.contiguous(), *ctx.saved_tensors, normalize=False), None
 
 
 class Dispatch(torch.autograd.Function):
@@ -95,12 +112,12 @@ class MoeLayer(torch.nn.Module):
     def forward(self, x, residual):
         """(layer output, new residual stream): [tokens, hidden] bf16 each."""
         q, scales, h, y = Norm.apply(x, residual, self.norm, self.eps)
-        probabilities, ids = torch.softmax(y.float() @ self.router, dim=1).topk(self.topk, dim=1)
-        slots, _, offsets = fq.fp8q_moe_sort(ids.contiguous(), self.experts)
+        weights, ids = Route.apply(y.float() @ self.router, self.topk)
+        slots, _, offsets = fq.fp8q_moe_sort(ids, self.experts)
         rows = Dispatch.apply(y, q, scales, slots)
         ends = offsets.tolist()                            # torch's matmul wants the runs on the host
         out = torch.cat([rows[ends[e]:ends[e + 1]] @ self.weights[e] for e in range(self.experts)])
-        return Combine.apply(out, slots, probabilities.contiguous()), h
+        return Combine.apply(out, slots, weights), h
 
 
 def main(argv=None):
@@ -108,6 +125,7 @@ def main(argv=None):
     p.add_argument("--tokens", type=int, default=512)
     p.add_argument("--hidden", type=int, default=256)
     p.add_argument("--steps", type=int, default=3)
+    p.add_argument("--max-norm", type=float, default=1.0)
     a = p.parse_args(argv)
     torch.manual_seed(0)
     layer = MoeLayer(a.hidden)
@@ -121,9 +139,12 @@ def main(argv=None):
         loss = (out.float() + h.float() - target).square().mean()
         optimizer.zero_grad()
         loss.backward()
+        grads = [w.grad for w in layer.parameters()]
+        sumsq = fq.fp8q_grad_sumsq(grads)                  # a sharded job adds it up over its ranks here
+        norm = fq.fp8q_grad_clip(grads, sumsq, a.max_norm)
         optimizer.step()
         losses.append(float(loss.detach()))
-        print("step %d loss %.5f" % (step, losses[-1]), flush=True)
+        print("step %d loss %.5f gradient norm %.4f" % (step, losses[-1], float(norm)), flush=True)
     return losses
 
 
