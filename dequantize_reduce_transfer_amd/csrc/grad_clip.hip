@@ -245,8 +245,9 @@ __device__ __forceinline__ void scale_chunk(const Chunk &c, float by) {
 }
 
 template <uint32_t TENSORS>
-__global__ __launch_bounds__(kThreads) void clip_kernel(const Table<false, TENSORS> t, uint32_t chunks, const double *sumsq,
-                                                        double max_norm, double eps, float *norm_out) {
+__global__ __launch_bounds__(kThreads) void clip_kernel(const Table<false, TENSORS> t, uint32_t chunks,
+                                                        const double *sumsq, double max_norm, double eps,
+                                                        float *norm_out) {
   const double norm = __builtin_sqrt(*sumsq);
   if (norm_out && blockIdx.x == 0 && threadIdx.x == 0) *norm_out = (float)norm;
   if (max_norm == (double)INFINITY) return;

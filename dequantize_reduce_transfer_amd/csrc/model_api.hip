@@ -63,7 +63,8 @@ Extent extent_of(const fp8q_expert_matrix &m, fp8q_row_format format, int expert
 }
 
 bool experts_sizes_ok(size_t tokens, int topk, int experts, size_t hidden, size_t inter, fp8q_out_dtype out_dtype) {
-  return experts >= 1 && experts <= FP8Q_MAX_EXPERTS && topk >= 1 && topk <= FP8Q_MAX_TOPK && tokens <= FP8Q_EXPERTS_MAX_PAIRS / (size_t)topk &&
+  return experts >= 1 && experts <= FP8Q_MAX_EXPERTS && topk >= 1 && topk <= FP8Q_MAX_TOPK &&
+         tokens <= FP8Q_EXPERTS_MAX_PAIRS / (size_t)topk &&
          hidden <= FP8Q_EXPERTS_MAX_SIZE && inter <= FP8Q_EXPERTS_MAX_SIZE &&
          (out_dtype == FP8Q_OUT_F32 || out_dtype == FP8Q_OUT_BF16);
 }

@@ -1,12 +1,20 @@
 // moe_experts.hip -- a whole MoE layer for a few tokens, from weights in the
 // codec's formats, on gfx950.
 //
-//   gate_up_kernel  h[p] = silu(gate_e x_t) * (up_e x_t) of every pair p
-//   down_kernel     out_t = sum over the token's pairs of weight * (down_e h[p])
+//   up to 24 pairs (kFewPairs):
+//     gate_up_kernel  h[p] = silu(gate_e x_t) * (up_e x_t) of every pair p
+//     down_kernel     out_t = sum over the token's pairs of weight * (down_e h[p])
+//   more:
+//     wide_kernel     h[p], and again y[p] = down_e h[p]
+//     combine_kernel  out_t = sum over the token's pairs of weight * y[p]
 //
-// Both read the rows of the experts that a token chose once, and little else:
+// The rows of the experts that a token chose are read once, and little else is:
 // at 8 of 128 experts of 2048 x 768 a token's MXFP8 rows are 39 MB, so HBM
-// bounds them for as long as an expert has few tokens.
+// bounds all of them for as long as an expert has few tokens.  The rows come in
+// non-temporally, which took 10% off 32 tokens (119 us to 107) and left one token
+// where it was.  Measured on MI355X, whole calls: that layer in MXFP8, one token
+// 17 us (its bytes at 6.5 TB/s: 6), 2 26 (12), 5 41 (26), 32 102 (84), 128 129
+// (96); 128 tokens through 2 of 8 experts of 4096 x 14336 in bf16 521 (434).
 //
 // Products are 16x16x32 bf16 matrix instructions: the tokens' rows are operand
 // A, 16 weight rows operand B, and both may take the k's of a chunk of 64 in
@@ -31,7 +39,11 @@ enum RowFormat : int { kBf16 = 0, kE4M3 = 1, kE5M2 = 2, kMx8 = 3 };   // fp8q_ro
 constexpr uint32_t kMaxPairs = 1024;     // FP8Q_EXPERTS_MAX_PAIRS
 constexpr int kGateUpWaves = 4;          // of a gate_up workgroup: they share the k's
 constexpr int kDownWaves = 8;            // of a down workgroup: they share the experts
-constexpr uint32_t kFewPairs = 24;       // pairs up to which one kernel multiplies and adds up
+// Pairs up to which one kernel multiplies by down and adds up.  At 8 of 128
+// experts of 2048 x 768, 16 pairs take 26 us this way and 31 the other, which is
+// a launch more; 32 pairs take 41 and 36, since a workgroup's waves walk over
+// four experts each here.
+constexpr uint32_t kFewPairs = 24;
 
 // The experts of pairs p[0 .. N), -1 where they have none (an id outside the
 // experts, or a pair that does not exist).  The ids' loads are on their way
@@ -107,7 +119,8 @@ __device__ __forceinline__ u32x4 load_up_to(const uint8_t *row, uint32_t at, uin
 // bytes [at, at + 256) of them; `width` bytes a row.
 //   DIRECT  rows and their length are multiples of 16 bytes: straight into LDS;
 //           otherwise through registers, which `commit` writes to LDS, so that
-//           several tiles' loads may be on their way together
+//           several tiles' loads may be on their way together (78 choices
+//           among 60 E4M3 experts of 1411 x 1000: 70 us, 2.3 TB/s)
 template <int R, bool DIRECT>
 struct TileLoad {
   u32x4 v[DIRECT ? 1 : R / 4];
@@ -201,7 +214,7 @@ struct Scales {
     w[1] = v.y;
   }
 
-  // Where the row ends inside the tile: behind its last block anything finite.
+  // Where the row ends inside the tile: behind its last block zeros.
   __device__ __forceinline__ void load_end(const uint8_t *row, uint32_t e, uint32_t k) {
     if constexpr (F == kMx8) {
       const uint32_t blocks = k / kMxBlock, at = e / kMxBlock;
@@ -218,7 +231,7 @@ struct Scales {
     } else if constexpr (F != kBf16) {
       const uint32_t *p = reinterpret_cast<const uint32_t *>(row);
       w[0] = p[e / kBlock];
-      w[1] = p[(k - 1) / kBlock];
+      w[1] = (k - 1) / kBlock > e / kBlock ? p[(k - 1) / kBlock] : 0u;
     }
   }
 
@@ -460,16 +473,20 @@ __device__ __forceinline__ void store_h(const Layer &a, uint32_t pair, uint32_t 
   }
 }
 
-template <int F, bool ALIGNED>
-using GateUpDot = Dot<F, 2, 16, 1, 1, false, ALIGNED>;
+// One tile of each at a time: two of each (64 KiB of LDS a workgroup, so two of
+// them a CU) took 90 us where this took 69, for 256 pairs; and eight waves that
+// share the k's 48 us where four took 40, for 2 pairs of rows of 4096.
+template <int F, bool DIRECT>
+using GateUpDot = Dot<F, 2, 16, 1, 1, false, DIRECT>;
 
-// h of up to 16 pairs of one expert, for 16 of its rows.
-template <int F, bool ALIGNED>
+// h of up to 16 pairs of one expert, for 16 of its rows, whose k's the waves
+// share.
+template <int F, bool DIRECT>
 __device__ __forceinline__ void gate_up_tile(const Layer &a, uint32_t e, uint32_t n0, const uint16_t *list,
                                              uint32_t count, uint8_t *lds) {
   const uint32_t lane = lane_id(), r = lane % 16u, q = lane / 16u, wid = uniform(threadIdx.x / kWave);
   const uint32_t n = n0 + r < a.inter ? n0 + r : a.inter - 1;
-  GateUpDot<F, ALIGNED> dot;
+  GateUpDot<F, DIRECT> dot;
   dot.k = a.hidden;
   dot.parts = 0;
   dot.count = a.inter - n0;
@@ -504,31 +521,31 @@ __device__ __forceinline__ void gate_up_tile(const Layer &a, uint32_t e, uint32_
   }
 }
 
-template <int F, bool ALIGNED>
+template <int F, bool DIRECT>
 __global__ __launch_bounds__(64 * kGateUpWaves) void gate_up_kernel(const Layer a) {
   __shared__ uint16_t list[kFewPairs];
-  __shared__ alignas(16) uint8_t lds[kGateUpWaves * GateUpDot<F, ALIGNED>::kLds];
+  __shared__ alignas(16) uint8_t lds[kGateUpWaves * GateUpDot<F, DIRECT>::kLds];
   const uint32_t n0 = blockIdx.x % a.groups * 16u;
   const Pairs pairs(a, blockIdx.x / a.groups, 0, kFewPairs, list);
   if (pairs.count == 0) return;
   __syncthreads();
   for (uint32_t m0 = 0; m0 < pairs.count; m0 += 16u) {
     if (m0) __syncthreads();
-    gate_up_tile<F, ALIGNED>(a, (uint32_t)pairs.e, n0, list + m0, pairs.count - m0 < 16u ? pairs.count - m0 : 16u, lds);
+    gate_up_tile<F, DIRECT>(a, (uint32_t)pairs.e, n0, list + m0, pairs.count - m0 < 16u ? pairs.count - m0 : 16u, lds);
   }
 }
 
-template <int F, int R, int TILES, int PARTS, bool ALIGNED>
-using DownDot = Dot<F, 1, R, TILES, PARTS, true, ALIGNED>;
+template <int F, int R, int TILES, int PARTS, bool DIRECT>
+using DownDot = Dot<F, 1, R, TILES, PARTS, true, DIRECT>;
 
 // The product of up to 16 pairs of one expert with R of its rows, over tiles
 // [t0, t1) of the k's.
-template <int F, int R, int TILES, int PARTS, bool ALIGNED>
+template <int F, int R, int TILES, int PARTS, bool DIRECT>
 __device__ __forceinline__ f32x4 down_tile(const Layer &a, uint32_t e, uint32_t n0, uint32_t pair, uint32_t t0,
                                            uint32_t t1, uint8_t *lds) {
   const uint32_t lane = lane_id(), r = lane % 16u;
   const uint32_t n = n0 + r % R < a.hidden ? n0 + r % R : a.hidden - 1;
-  DownDot<F, R, TILES, PARTS, ALIGNED> dot;
+  DownDot<F, R, TILES, PARTS, DIRECT> dot;
   dot.k = a.inter;
   dot.parts = (uint64_t)a.pairs * a.padded;
   dot.count = a.hidden - n0;
@@ -548,14 +565,15 @@ __device__ __forceinline__ void store_out(const Layer &a, uint64_t at, float v) 
     static_cast<float *>(a.out)[at] = v;
 }
 
-// Up to 64 pairs: a workgroup takes R rows of every expert that a pair names,
-// the waves an expert (or a part of its k's) each, and adds the pairs up.
-template <int F, int R, int PARTS, bool ALIGNED>
+// Up to kFewPairs pairs: a workgroup takes R rows of every expert that a pair
+// names, the waves an expert (or a part of its k's) each, and adds the pairs up.
+// R is 8 where 16 would leave CUs without a workgroup (hidden < 4096).
+template <int F, int R, int PARTS, bool DIRECT>
 __global__ __launch_bounds__(64 * kDownWaves) void down_kernel(const Layer a) {
   constexpr int kTiles = PARTS == 3 ? 1 : 3;       // what the registers hold
   __shared__ float y[kDownWaves * kFewPairs * R];  // [split][pair][row]
   __shared__ float weights[kFewPairs];
-  __shared__ alignas(16) uint8_t tiles[kDownWaves * DownDot<F, R, kTiles, PARTS, ALIGNED>::kLds];
+  __shared__ alignas(16) uint8_t tiles[kDownWaves * DownDot<F, R, kTiles, PARTS, DIRECT>::kLds];
   const uint32_t tid = threadIdx.x, lane = lane_id(), wid = uniform(tid / kWave);
   const uint32_t pairs = a.pairs, n0 = blockIdx.x * (uint32_t)R, r = lane % 16u, q = lane / 16u;
   // lane p's pair: the others of its expert, and whether it is their first
@@ -589,8 +607,9 @@ __global__ __launch_bounds__(64 * kDownWaves) void down_kernel(const Layer a) {
         const uint32_t p = (uint32_t)__builtin_ctzll(mine);
         pair = r >= c ? p : pair;
       }
-      const f32x4 sums = down_tile<F, R, kTiles, PARTS, ALIGNED>(
-          a, x, n0, pair, whole * s / splits, whole * (s + 1) / splits, tiles + wid * DownDot<F, R, kTiles, PARTS, ALIGNED>::kLds);
+      const f32x4 sums = down_tile<F, R, kTiles, PARTS, DIRECT>(
+          a, x, n0, pair, whole * s / splits, whole * (s + 1) / splits,
+          tiles + wid * DownDot<F, R, kTiles, PARTS, DIRECT>::kLds);
 #pragma unroll
       for (uint32_t i = 0; i < 4; ++i) {
         const uint32_t to = (uint32_t)__shfl((int)pair, (int)(4u * q + i));
@@ -642,10 +661,16 @@ __global__ __launch_bounds__(256) void combine_kernel(const Layer a) {
   if (column < a.hidden) store_out(a, (uint64_t)blockIdx.y * a.hidden + column, sum);
 }
 
-// Many tokens an expert: the workgroup's waves take 16 rows each of gate and of
-// up (or twice 16 of down), and share the tokens' rows, which go through LDS as
-// the weights do: straight from memory into registers, 16 tokens are 16 rows a
-// load.
+// More pairs: the workgroup's waves take 16 rows each of gate and of up (or twice
+// 16 of down), over all of the k's, and share the tokens' rows, which go through
+// LDS as the weights do: straight from memory into registers, 16 tokens are 16
+// rows a load.  For 128 tokens of 2 of 8 wide bf16 experts the kernels above,
+// which do that, took 1239 us, and 639 went through these; 32 tokens of 8 of 128,
+// two an expert, 135 and 119.
+//
+// While a workgroup multiplies, its loads' place in LDS is taken, and the CU's
+// other workgroups load: small ones do better than large ones (eight waves that
+// share the tokens: 142 us for 119, 759 for 639).
 constexpr int kWideWaves = 4;
 
 template <int F, int M, int PARTS>
@@ -763,11 +788,11 @@ struct WideDot {
 };
 
 // h of `count` pairs of one expert, up to 16 M, for the workgroup's 64 rows of
-// gate and up from n0 on, or their y for its 128 rows of down.  `list`, which
-// holds them, is in tokens_lds.
+// gate and up from n0 on, or their y for its 128 rows of down, over part `split`
+// of the k's.  `list`, which holds them, is in tokens_lds.
 template <int F, bool DOWN, int M, int PARTS, bool DIRECT>
-__device__ __forceinline__ void wide_tile(const Layer &a, uint32_t e, uint32_t n0, uint32_t split, uint16_t *list, uint32_t count,
-                                          uint8_t *weights_lds, uint8_t *tokens_lds) {
+__device__ __forceinline__ void wide_tile(const Layer &a, uint32_t e, uint32_t n0, uint32_t split, uint16_t *list,
+                                          uint32_t count, uint8_t *weights_lds, uint8_t *tokens_lds) {
   const uint32_t lane = lane_id(), r = lane % 16u, q = lane / 16u, wid = uniform(threadIdx.x / kWave);
   const uint32_t rows = DOWN ? a.hidden : a.inter, k = DOWN ? a.inter : a.hidden;
   WideDot<F, M, PARTS, DOWN, DIRECT> dot;
@@ -847,7 +872,7 @@ bool aligned_rows(const ExpertMatrix &m, uint32_t k) {
 
 // Parts of down's k's.  Where the experts' rows alone would not give every CU
 // four workgroups, parts of 1024 k's or more do (256 workgroups of 14336 k's,
-// 128 tokens: one part 246 us, four 1SPLIT us).
+// 128 tokens: one part 246 us, four 189, and 4 more in the sum).
 uint32_t splits_of(uint32_t pairs, uint32_t experts, uint32_t hidden, uint32_t inter) {
   const uint32_t workgroups = (pairs < experts ? pairs : experts) * ((hidden + 127u) / 128u);
   const uint32_t want = 1024u / workgroups, most = inter / 1024u;
@@ -900,7 +925,10 @@ hipError_t down(const Layer &a, int wide, hipStream_t stream) {
   return hipGetLastError();
 }
 
-// 0: few pairs; else how many times 16 tokens the wide kernels hold.
+// 0: few pairs; else how many times 16 tokens the wide kernels hold, which have
+// to be few for an expert's share of the pairs, since room for more takes LDS and
+// registers from the loads: at 8 pairs an expert 16 take 156 us, 32 168 and 64
+// 204; at 32 pairs (wide bf16 experts) 16 take 1339, 32 859 and 64 639.
 int wide_of(uint32_t pairs, uint32_t experts) {
   if (pairs <= kFewPairs) return 0;
   const uint32_t each = (pairs + experts - 1) / experts;
@@ -911,7 +939,8 @@ template <int F>
 hipError_t experts_launch(const MoeExperts &m, hipStream_t stream) {
   const uint32_t pairs = m.tokens * m.topk;
   const Layer a{m.x, m.ids, m.weights, m.ids64, m.out_bf16, pairs < m.experts, m.tokens, m.topk, pairs,
-                m.inter ? m.experts : 0, m.hidden, m.inter, padded(m.inter), 0, splits_of(pairs, m.experts, m.hidden, m.inter), m.gate, m.up, m.down, m.workspace,
+                m.inter ? m.experts : 0, m.hidden, m.inter, padded(m.inter), 0,
+                splits_of(pairs, m.experts, m.hidden, m.inter), m.gate, m.up, m.down, m.workspace,
                 reinterpret_cast<float *>(m.workspace + h_bytes(pairs, m.inter, m.out_bf16) / 2), m.out};
   const int wide = m.inter ? wide_of(pairs, m.experts) : 0;
   if (m.inter) {

@@ -102,7 +102,9 @@ typedef struct {
  * and other pairs (padding, or an expert that lives elsewhere) are left out: a
  * token without any gets zeros.  The weights' values are exact (a code times
  * its scale is not rounded), products are summed in fp32, and g, u, h and y
- * are fp32 values; for bf16 output h is held to 16 bits, as two bf16 numbers.
+ * are fp32 values; for bf16 output h is held to 15 bits or more, as two bf16
+ * numbers.  Values under 2^-126 in magnitude (of x, weights and h) may be taken
+ * as zero.
  * The same expert may be chosen twice by one token.  The same call gives the
  * same bits.  tokens == 0 or hidden == 0 is a successful no-op; with inter == 0
  * out is zeros.
