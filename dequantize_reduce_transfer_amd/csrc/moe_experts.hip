@@ -673,8 +673,16 @@ __global__ __launch_bounds__(256) void combine_kernel(const Layer a) {
 // share the tokens: 142 us for 119, 759 for 639).
 constexpr int kWideWaves = 4;
 
+// Of 16 M tokens, 16 times those whose rows are in LDS at once.  Where half of
+// them leave room for a workgroup more a CU, and their registers do too, the
+// weights are multiplied with one half after the other (gate and up of wide bf16
+// experts, 128 tokens: 375 us whole, 350 in halves; down 190 and 212, MXFP8 212
+// and 219).
 template <int F, int M, int PARTS>
-constexpr uint32_t kTokenBytes = PARTS * M * 16 * 2 * kTile<F>;
+constexpr int kHeldTiles = M > 2 && F == kBf16 && PARTS == 1 ? 2 : M;
+
+template <int F, int M, int PARTS>
+constexpr uint32_t kTokenBytes = PARTS * kHeldTiles<F, M, PARTS> * 16 * 2 * kTile<F>;
 
 // sums[n][m] = products of the wave's rows (rows[n]: the first one's, scales[n]:
 // the lane's one's) with 16 M tokens' rows.
@@ -692,17 +700,20 @@ struct WideDot {
   static constexpr uint32_t kPieces = 2 * kTile<F> / 16;
   static constexpr uint32_t kUnits = kTokenBytes<F, M, PARTS> / 1024;
   static constexpr uint32_t kLoads = (kUnits + kWideWaves - 1) / kWideWaves;   // a wave's
-  uint32_t from[kLoads];                                 // the lane's rows' bytes into `tokens`, one a load
+  static constexpr int kHeld = kHeldTiles<F, M, PARTS>, kRounds = M / kHeld;
+  uint32_t from[kRounds][kLoads];                        // the lane's rows' bytes into `tokens`, one a load
 
   // list: the pairs (all 16 M); a pair's row is pair / per * stride bytes into
   // `tokens`, its parts part_bytes apart.
   __device__ __forceinline__ void find(const uint16_t *list, uint32_t count, uint32_t per, uint32_t stride,
                                        uint32_t part_bytes, uint32_t lane, uint32_t wid) {
 #pragma unroll
-    for (uint32_t i = 0; i < kLoads; ++i) {
-      const uint32_t row = ((wid * kLoads + i) * 64u + lane) / kPieces, c = row % (16u * M);
-      from[i] = list[c < count ? c : count - 1] / per * stride + row / (16u * M) * part_bytes;
-    }
+    for (int h = 0; h < kRounds; ++h)
+#pragma unroll
+      for (uint32_t i = 0; i < kLoads; ++i) {
+        const uint32_t row = ((wid * kLoads + i) * 64u + lane) / kPieces, c = h * 16u * kHeld + row % (16u * kHeld);
+        from[h][i] = list[c < count ? c : count - 1] / per * stride + row / (16u * kHeld) * part_bytes;
+      }
   }
 
   template <bool END>
@@ -722,58 +733,63 @@ struct WideDot {
     }
     constexpr bool kTokensDirect = PADDED || DIRECT;     // rows are multiples of 16 bytes
     const uint32_t end = 2u * (PADDED ? (k + 15u) / 16u * 16u : k);
-    u32x4 v[kTokensDirect ? 1 : kLoads];
+    const u32x4 zero = {0u, 0u, 0u, 0u};
 #pragma unroll
-    for (uint32_t i = 0; i < kLoads; ++i) {
-      if (kUnits % kWideWaves && wid * kLoads + i >= kUnits) break;
-      const uint32_t unit = (wid * kLoads + i) * 64u + lane, row = unit / kPieces, c = row % (16u * M);
-      const uint32_t p = (unit % kPieces) ^ (c % 16u), b = 2u * e + p * 16u;
-      const uint8_t *row_at = tokens + from[i];
-      if constexpr (kTokensDirect)
-        __builtin_amdgcn_global_load_lds((GlobalPtr)(row_at + (!END || b < end ? b : 0u)),
-                                         (LdsPtr)(tokens_lds + (wid * kLoads + i) * 1024u), 16, 0, 0);
-      else
-        v[i] = END ? load_up_to(row_at, b, end) : load16<false>(row_at + b);
-    }
-    loads_issued();
+    for (int h = 0; h < kRounds; ++h) {
+      u32x4 v[kTokensDirect ? 1 : kLoads];
 #pragma unroll
-    for (int n = 0; n < 2; ++n) loads[n].commit(weights_lds + n * 4096, lane);
-    if constexpr (!kTokensDirect) {
-#pragma unroll
-      for (uint32_t i = 0; i < kLoads; ++i)
-        if (kUnits % kWideWaves == 0 || wid * kLoads + i < kUnits)
-          *reinterpret_cast<u32x4 *>(tokens_lds + (wid * kLoads + i) * 1024u + lane * 16u) = v[i];
-    }
-    all_loaded();
-    __syncthreads();
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      u32x4 x[2];
-#pragma unroll
-      for (int n = 0; n < 2; ++n) {
-        x[n] = read_piece<16>(weights_lds + n * 4096, c, r, q);
-        if (END && DIRECT && at + (c * 4u + q) * 16u >= width) x[n] = u32x4{0u, 0u, 0u, 0u};
+      for (uint32_t i = 0; i < kLoads; ++i) {
+        if (kUnits % kWideWaves && wid * kLoads + i >= kUnits) break;
+        const uint32_t unit = (wid * kLoads + i) * 64u + lane;
+        const uint32_t p = (unit % kPieces) ^ (unit / kPieces % 16u), b = 2u * e + p * 16u;
+        const uint8_t *row_at = tokens + from[h][i];
+        if constexpr (kTokensDirect)
+          __builtin_amdgcn_global_load_lds((GlobalPtr)(row_at + (!END || b < end ? b : 0u)),
+                                           (LdsPtr)(tokens_lds + (wid * kLoads + i) * 1024u), 16, 0, 0);
+        else
+          v[i] = END ? load_up_to(row_at, b, end) : load16<false>(row_at + b);
       }
-      const Weights<F> w[2] = {{x[0], s[0].of(c, q)}, {x[1], s[1].of(c, q)}};
+      loads_issued();
+      if (h == 0) {
 #pragma unroll
-      for (int m = 0; m < M; ++m) {
-        Operand<F, PARTS> t;
-#pragma unroll
-        for (int i = 0; i < PARTS; ++i)
-#pragma unroll
-          for (int j = 0; j < kVectors<F>; ++j) {
-            const uint32_t p = (c * 4u + q) * kVectors<F> + j;
-            u32x4 v = *reinterpret_cast<const u32x4 *>(
-                tokens_lds + ((i * M + m) * 16u + r) * (kPieces * 16u) + ((p ^ r) * 16u));
-            if (END && kTokensDirect && 2u * e + p * 16u >= end) v = u32x4{0u, 0u, 0u, 0u};
-            t.v[i][j] = v;
-          }
-#pragma unroll
-        for (int n = 0; n < 2; ++n) multiply<F, PARTS>(sums[n][m], t, w[n]);
-        if (m % 2 || m + 1 == M) loads_issued();
+        for (int n = 0; n < 2; ++n) loads[n].commit(weights_lds + n * 4096, lane);
       }
+      if constexpr (!kTokensDirect) {
+#pragma unroll
+        for (uint32_t i = 0; i < kLoads; ++i)
+          if (kUnits % kWideWaves == 0 || wid * kLoads + i < kUnits)
+            *reinterpret_cast<u32x4 *>(tokens_lds + (wid * kLoads + i) * 1024u + lane * 16u) = v[i];
+      }
+      all_loaded();
+      __syncthreads();
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        u32x4 x[2];
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          x[n] = read_piece<16>(weights_lds + n * 4096, c, r, q);
+          if (END && DIRECT && at + (c * 4u + q) * 16u >= width) x[n] = zero;
+        }
+        const Weights<F> w[2] = {{x[0], s[0].of(c, q)}, {x[1], s[1].of(c, q)}};
+#pragma unroll
+        for (int m = 0; m < kHeld; ++m) {
+          Operand<F, PARTS> t;
+#pragma unroll
+          for (int i = 0; i < PARTS; ++i)
+#pragma unroll
+            for (int j = 0; j < kVectors<F>; ++j) {
+              const uint32_t p = (c * 4u + q) * kVectors<F> + j;
+              t.v[i][j] = *reinterpret_cast<const u32x4 *>(
+                  tokens_lds + ((i * kHeld + m) * 16u + r) * (kPieces * 16u) + ((p ^ r) * 16u));
+              if (END && kTokensDirect && 2u * e + p * 16u >= end) t.v[i][j] = zero;
+            }
+#pragma unroll
+          for (int n = 0; n < 2; ++n) multiply<F, PARTS>(sums[n][h * kHeld + m], t, w[n]);
+        }
+        loads_issued();
+      }
+      __syncthreads();                                   // before the next loads overwrite these
     }
-    __syncthreads();                                     // before the next stage's loads overwrite these
   }
 
   // over tiles [t0, t1) of the rows
