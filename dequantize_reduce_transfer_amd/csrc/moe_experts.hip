@@ -99,12 +99,11 @@ __host__ __device__ __forceinline__ uint64_t scale_bytes(uint32_t k) {
   return F == kBf16 ? 0 : F == kMx8 ? k / kMxBlock : 4ull * ((k + kBlock - 1) / kBlock);
 }
 
-// Bytes [at, at + 16) of a row, zeros past its end.
-__device__ __forceinline__ u32x4 load_up_to(const uint8_t *row, uint32_t at, uint32_t bytes) {
-  if (bytes >= 16u) {
-    const uint32_t from = at + 16u <= bytes ? at : bytes - 16u;
-    return shift_down(load16<false>(row + from), at - from, 8);
-  }
+// Bytes [at, at + 16) of a row, zeros past its end, in two steps: the load, from
+// inside the row, and what it takes afterwards (so that several loads are on
+// their way before the first is waited for).
+__device__ __forceinline__ u32x4 load_end(const uint8_t *row, uint32_t at, uint32_t bytes) {
+  if (bytes >= 16u) return load16<false>(row + (at + 16u <= bytes ? at : bytes - 16u));
   u32x4 v = {0u, 0u, 0u, 0u};
 #pragma unroll 1
   for (uint32_t j = 0; at + j < bytes; ++j) {
@@ -113,6 +112,12 @@ __device__ __forceinline__ u32x4 load_up_to(const uint8_t *row, uint32_t at, uin
     for (uint32_t i = 0; i < 4; ++i) v[i] |= j / 4 == i ? byte : 0u;
   }
   return v;
+}
+__device__ __forceinline__ u32x4 take_end(u32x4 v, uint32_t at, uint32_t bytes) {
+  return shift_down(v, bytes < 16u || at + 16u <= bytes ? 0u : at + 16u - bytes, 8);
+}
+__device__ __forceinline__ u32x4 load_up_to(const uint8_t *row, uint32_t at, uint32_t bytes) {
+  return take_end(load_end(row, at, bytes), at, bytes);
 }
 
 // The loads of a tile: rows [0, R) (those from `rows` on: the last row again) and
@@ -152,14 +157,19 @@ struct TileLoad {
         __builtin_amdgcn_global_load_lds((GlobalPtr)(from + (b < width ? b : width - 16u)), (LdsPtr)(tile + i * 1024),
                                          16, 0, 2);
       else
-        v[i] = load_up_to(from, b, width);
+        v[i] = load_end(from, b, width);
     }
   }
 
-  __device__ __forceinline__ void commit(uint8_t *tile, uint32_t lane) const {
+  // END: after issue_end, of the same rows and bytes.
+  template <bool END>
+  __device__ __forceinline__ void commit(uint8_t *tile, uint32_t width, uint32_t at, uint32_t lane) const {
     if constexpr (!DIRECT) {
 #pragma unroll
-      for (uint32_t i = 0; i < R / 4; ++i) *reinterpret_cast<u32x4 *>(tile + i * 1024 + lane * 16u) = v[i];
+      for (uint32_t i = 0; i < R / 4; ++i) {
+        const uint32_t b = at + ((lane % 16u) ^ (i * 4 + lane / 16u)) * 16u;
+        *reinterpret_cast<u32x4 *>(tile + i * 1024 + lane * 16u) = END ? take_end(v[i], b, width) : v[i];
+      }
     }
   }
 };
@@ -231,7 +241,8 @@ struct Scales {
     } else if constexpr (F != kBf16) {
       const uint32_t *p = reinterpret_cast<const uint32_t *>(row);
       w[0] = p[e / kBlock];
-      w[1] = (k - 1) / kBlock > e / kBlock ? p[(k - 1) / kBlock] : 0u;
+      const uint32_t last = p[(k - 1) / kBlock];
+      w[1] = (k - 1) / kBlock > e / kBlock ? last : 0u;
     }
   }
 
@@ -357,7 +368,8 @@ struct Dot {
 #pragma unroll
     for (int w = 0; w < W; ++w)
 #pragma unroll
-      for (int n = 0; n < N; ++n) loads[w][n].commit(tile(w, n), lane);
+      for (int n = 0; n < N; ++n)
+        loads[w][n].template commit<END>(tile(w, n), width, (uint32_t)row_bytes<F>(e + w * kTile<F>), lane);
     all_loaded();
     if (!DIRECT) lds_done();
 #pragma unroll
@@ -747,18 +759,21 @@ struct WideDot {
           __builtin_amdgcn_global_load_lds((GlobalPtr)(row_at + (!END || b < end ? b : 0u)),
                                            (LdsPtr)(tokens_lds + (wid * kLoads + i) * 1024u), 16, 0, 0);
         else
-          v[i] = END ? load_up_to(row_at, b, end) : load16<false>(row_at + b);
+          v[i] = END ? load_end(row_at, b, end) : load16<false>(row_at + b);
       }
       loads_issued();
       if (h == 0) {
 #pragma unroll
-        for (int n = 0; n < 2; ++n) loads[n].commit(weights_lds + n * 4096, lane);
+        for (int n = 0; n < 2; ++n) loads[n].template commit<END>(weights_lds + n * 4096, width, at, lane);
       }
       if constexpr (!kTokensDirect) {
 #pragma unroll
-        for (uint32_t i = 0; i < kLoads; ++i)
+        for (uint32_t i = 0; i < kLoads; ++i) {
+          const uint32_t unit = (wid * kLoads + i) * 64u + lane;
+          const uint32_t b = 2u * e + ((unit % kPieces) ^ (unit / kPieces % 16u)) * 16u;
           if (kUnits % kWideWaves == 0 || wid * kLoads + i < kUnits)
-            *reinterpret_cast<u32x4 *>(tokens_lds + (wid * kLoads + i) * 1024u + lane * 16u) = v[i];
+            *reinterpret_cast<u32x4 *>(tokens_lds + unit * 16u) = END ? take_end(v[i], b, end) : v[i];
+        }
       }
       all_loaded();
       __syncthreads();
