@@ -224,7 +224,7 @@ struct Scales {
     w[1] = v.y;
   }
 
-  // Where the row ends inside the tile: behind its last block zeros.
+  // Where the row ends inside the tile: what is behind is not used.
   __device__ __forceinline__ void load_end(const uint8_t *row, uint32_t e, uint32_t k) {
     if constexpr (F == kMx8) {
       const uint32_t blocks = k / kMxBlock, at = e / kMxBlock;
@@ -241,13 +241,18 @@ struct Scales {
     } else if constexpr (F != kBf16) {
       const uint32_t *p = reinterpret_cast<const uint32_t *>(row);
       w[0] = p[e / kBlock];
-      const uint32_t last = p[(k - 1) / kBlock];
-      w[1] = (k - 1) / kBlock > e / kBlock ? last : 0u;
+      w[1] = p[(k - 1) / kBlock];
     }
   }
 
   __device__ __forceinline__ float of(int c, uint32_t q) const {
     return scale_of<F>(F == kMx8 ? w[c / 2] >> (16 * (c % 2) + 8 * (q / 2u)) : w[c / 2]);
+  }
+
+  // Of a tile at element e in which the row ends: 0 for a chunk behind it, whose
+  // products' sum, 0 too, an infinite scale would make a NaN.
+  __device__ __forceinline__ float of_end(int c, uint32_t q, uint32_t e, uint32_t k) const {
+    return (F == kE4M3 || F == kE5M2) && e + c * 4u * kPiece<F> >= k ? 0.0f : of(c, q);
   }
 };
 
@@ -380,7 +385,7 @@ struct Dot {
         for (int n = 0; n < N; ++n) {
           u32x4 v = read_piece<R>(tile(w, n), c, r, q);
           if (END && DIRECT && (uint32_t)row_bytes<F>(e) + (c * 4u + q) * 16u >= width) v = u32x4{0u, 0u, 0u, 0u};
-          multiply<F, PARTS>(sums[n], t[W > 1 ? w % 2 : 0][c], Weights<F>(v, s[n][w].of(c, q)));
+          multiply<F, PARTS>(sums[n], t[W > 1 ? w % 2 : 0][c], Weights<F>(v, END ? s[n][w].of_end(c, q, e, k) : s[n][w].of(c, q)));
         }
         loads_issued();
       }
@@ -785,7 +790,8 @@ struct WideDot {
           x[n] = read_piece<16>(weights_lds + n * 4096, c, r, q);
           if (END && DIRECT && at + (c * 4u + q) * 16u >= width) x[n] = zero;
         }
-        const Weights<F> w[2] = {{x[0], s[0].of(c, q)}, {x[1], s[1].of(c, q)}};
+        const Weights<F> w[2] = {{x[0], END ? s[0].of_end(c, q, e, k) : s[0].of(c, q)},
+                                 {x[1], END ? s[1].of_end(c, q, e, k) : s[1].of(c, q)}};
 #pragma unroll
         for (int m = 0; m < kHeld; ++m) {
           Operand<F, PARTS> t;

@@ -268,6 +268,31 @@ def test_special_values_stay_with_their_tokens_and_rows(fmt):
     assert not got[2:4].isfinite().any() and torch.equal(got[[0, 1, 6, 7]], clean[[0, 1, 6, 7]])
 
 
+@pytest.mark.parametrize("tokens", [2, 40])
+@pytest.mark.parametrize("inter", [300, 416])
+def test_an_infinite_scale_of_a_row_s_last_block(inter, tokens):
+    """The output that the block is part of is infinite, and no NaN comes from
+    the k's behind the row's end."""
+    layer = Layer(E4M3, 2, 64, inter, 1)
+    x, ids, w = tokens_of(tokens, 1, 2, 64, 3)
+    ids[:] = 1
+    clean = layer(x, ids, w)
+    layer.s["down"].view(2, 64, -1)[1, 10, -1] = float("inf")
+    got = layer(x, ids, w)
+    assert got[:, 10].isinf().all()
+    got[:, 10] = clean[:, 10]
+    assert torch.equal(got, clean)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_wide_rows_of_few_tokens(fmt):
+    """Sixteen rows of down a workgroup (hidden from 4096 on), the last partial."""
+    hidden = 4128 if fmt == MX8 else 4101
+    layer = Layer(fmt, 3, hidden, 64, 2)
+    for dtype in (torch.bfloat16, torch.float32):
+        check(layer, *tokens_of(2, 2, 3, hidden, 1), dtype)
+
+
 def test_scales_at_the_ends_of_e8m0():
     """Scales of 2^-127 and 2^127 as the codec decodes them."""
     layer = Layer(MX8, 2, 64, 32, 1)
