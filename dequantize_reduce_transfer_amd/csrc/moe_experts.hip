@@ -7,6 +7,7 @@
 //   more:
 //     wide_kernel     h[p], and again y[p] = down_e h[p]
 //     combine_kernel  out_t = sum over the token's pairs of weight * y[p]
+//   inter == 0: combine_kernel alone, of any number of pairs and no expert
 //
 // The rows of the experts that a token chose are read once, and little else is:
 // at 8 of 128 experts of 2048 x 768 a token's MXFP8 rows are 39 MB, so HBM
@@ -583,7 +584,7 @@ __device__ __forceinline__ void store_out(const Layer &a, uint64_t at, float v) 
     static_cast<float *>(a.out)[at] = v;
 }
 
-// Up to kFewPairs pairs: a workgroup takes R rows of every expert that a pair
+// Up to kFewPairs pairs, no more: a workgroup takes R rows of every expert that a pair
 // names, the waves an expert (or a part of its k's) each, and adds the pairs up.
 // R is 8 where 16 would leave CUs without a workgroup (hidden < 4096).
 template <int F, int R, int PARTS, bool DIRECT>
@@ -947,6 +948,11 @@ hipError_t gate_up(const Layer &a, int wide, hipStream_t stream) {
   return by_expert(gate_up_kernel<F, DIRECT>, a, (a.inter + 15u) / 16u, 1, kGateUpWaves, stream);
 }
 
+hipError_t combine(const Layer &a, hipStream_t stream) {
+  hipLaunchKernelGGL(combine_kernel, dim3((a.hidden + 255u) / 256u, a.tokens), dim3(256), 0, stream, a);
+  return hipGetLastError();
+}
+
 template <int F, int PARTS, bool DIRECT>
 hipError_t down(const Layer &a, int wide, hipStream_t stream) {
   if (!wide) {
@@ -958,9 +964,7 @@ hipError_t down(const Layer &a, int wide, hipStream_t stream) {
     return hipGetLastError();
   }
   const hipError_t e = wide_launch<F, true, PARTS, DIRECT>(a, wide, stream);
-  if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(combine_kernel, dim3((a.hidden + 255u) / 256u, a.tokens), dim3(256), 0, stream, a);
-  return hipGetLastError();
+  return e != hipSuccess ? e : combine(a, stream);
 }
 
 // 0: few pairs; else how many times 16 tokens the wide kernels hold, which have
@@ -980,12 +984,11 @@ hipError_t experts_launch(const MoeExperts &m, hipStream_t stream) {
                 m.inter ? m.experts : 0, m.hidden, m.inter, padded(m.inter), 0,
                 splits_of(pairs, m.experts, m.hidden, m.inter), m.gate, m.up, m.down, m.workspace,
                 reinterpret_cast<float *>(m.workspace + h_bytes(pairs, m.inter, m.out_bf16) / 2), m.out};
-  const int wide = m.inter ? wide_of(pairs, m.experts) : 0;
-  if (m.inter) {
-    const bool direct = aligned_rows<F>(m.gate, m.hidden) && aligned_rows<F>(m.up, m.hidden);
-    const hipError_t e = direct ? gate_up<F, true>(a, wide, stream) : gate_up<F, false>(a, wide, stream);
-    if (e != hipSuccess) return e;
-  }
+  if (!m.inter) return combine(a, stream);                // of no experts: zeros, and no y is read
+  const int wide = wide_of(pairs, m.experts);
+  const bool gate_up_direct = aligned_rows<F>(m.gate, m.hidden) && aligned_rows<F>(m.up, m.hidden);
+  const hipError_t e = gate_up_direct ? gate_up<F, true>(a, wide, stream) : gate_up<F, false>(a, wide, stream);
+  if (e != hipSuccess) return e;
   const bool direct = aligned_rows<F>(m.down, m.inter);
   if (m.out_bf16) return direct ? down<F, 2, true>(a, wide, stream) : down<F, 2, false>(a, wide, stream);
   return direct ? down<F, 3, true>(a, wide, stream) : down<F, 3, false>(a, wide, stream);

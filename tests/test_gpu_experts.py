@@ -383,3 +383,17 @@ def test_refusals():
                             l.t["down"].to(torch.uint8), gate_scales=s["gate"], up_scales=s["up"], down_scales=s["down"])
     with pytest.raises(fq.Fp8qError):
         call(out=x)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("tokens,topk", [(24, 1), (25, 1), (13, 5), (75, 8), (16, 64), (1024, 1)])
+def test_experts_without_rows_give_zeros(fmt, tokens, topk):
+    """inter == 0 with few pairs and many, up to the most that there may be."""
+    layer = Layer(fmt, 70, 96, 0, 1)
+    x, ids, w = tokens_of(tokens, topk, 70, 96, 2, gone=0.1)
+    w[0] = float("nan")                     # times no y
+    assert fq.fp8q_moe_experts_workspace(tokens, topk, 70, 96, 0) == 0
+    for dtype in (torch.bfloat16, torch.float32):
+        buffer = torch.full((tokens + 1, 96), 3.0, device=x.device, dtype=dtype)
+        layer(x, ids, w, out_dtype=dtype, out=buffer[:tokens])
+        assert not buffer[:tokens].view(torch.uint8).any() and (buffer[tokens] == 3).all()
