@@ -397,3 +397,77 @@ def test_experts_without_rows_give_zeros(fmt, tokens, topk):
         buffer = torch.full((tokens + 1, 96), 3.0, device=x.device, dtype=dtype)
         layer(x, ids, w, out_dtype=dtype, out=buffer[:tokens])
         assert not buffer[:tokens].view(torch.uint8).any() and (buffer[tokens] == 3).all()
+
+
+def at_an_odd_address(t):
+    """A copy that begins as far off 16 bytes as its type allows."""
+    wide = torch.empty(t.numel() + 1, dtype=t.dtype, device=t.device)
+    wide[1:] = t.reshape(-1)
+    return wide[1:].view(t.shape)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("hidden,inter", [(256, 512), (160, 96), (32, 2144)])
+@pytest.mark.parametrize("tokens", [2, 9, 40, 200])
+def test_rows_at_any_address(fmt, hidden, inter, tokens):
+    """The same bits from matrices that do not begin at a multiple of 16 bytes,
+    all three of them or one."""
+    layer = Layer(fmt, 3, hidden, inter, 5)
+    x, ids, w = tokens_of(tokens, 2, 3, hidden, tokens, gone=0.1)
+    for dtype in (torch.bfloat16, torch.float32):
+        want = check(layer, x, ids, w, dtype)
+        for moved in (("gate", "up", "down"), ("gate",), ("up",), ("down",)):
+            other = Layer.__new__(Layer)
+            other.fmt, other.s = fmt, dict(layer.s)
+            other.t = {k: at_an_odd_address(t) if k in moved else t for k, t in layer.t.items()}
+            assert all(other.t[k].data_ptr() % 16 for k in moved)
+            if fmt == MX8:
+                other.s = {k: at_an_odd_address(s) if k in moved else s for k, s in layer.s.items()}
+            assert torch.equal(other(x, ids, w, out_dtype=dtype), want), moved
+
+
+@pytest.mark.parametrize("tokens", [2, 40])
+@pytest.mark.parametrize("name", ["gate", "up", "down"])
+def test_a_block_of_the_smallest_e8m0_scale(name, tokens):
+    """Codes of 8 and more times 2^-127 are past 2^-126: their values count.
+    Another matrix's 2^60 keeps what comes of them far from there."""
+    layer = Layer(MX8, 2, 64, 32, 1)
+    x, ids, w = tokens_of(tokens, 1, 2, 64, 3)
+    x = torch.where(x < 0, x - 1, x + 1)
+    rng = np.random.default_rng(4)
+    other = "down" if name == "up" else "up"
+    layer.s[other] += 60
+    layer.v[other] = layer.v[other] * 2.0 ** 60
+    rows, width = layer.t[name].shape[1:]
+    codes = (rng.integers(0x50, 0x7F, size=(rows, width)) | rng.integers(0, 2, size=(rows, width)) << 7).astype(np.uint8)
+    layer.t[name][0] = torch.from_numpy(codes).to(x.device)
+    layer.s[name].view(2, rows, -1)[0] = 0
+    layer.v[name][0] = oracle.fp8_decode(codes, 0).astype(np.float64) * 2.0 ** -127
+    for dtype in (torch.bfloat16, torch.float32):
+        got = check(layer, x, ids, w, dtype)
+        assert bool((got[ids[:, 0] == 0] != 0).all())
+
+
+@pytest.mark.parametrize("tokens", [2, 40])
+def test_mx8_values_past_fp32_are_infinite(tokens):
+    """As mx8_dequantize decodes them; the largest below keeps its value."""
+    layer = Layer(MX8, 2, 64, 32, 1)
+    x, ids, w = tokens_of(tokens, 1, 2, 64, 3)
+    ids[:] = 0
+    clean = layer(x, ids, w, out_dtype=torch.float32)
+    layer.t["down"][0, 10:12] = 0
+    layer.t["down"][0, 10, 3] = 0x7E        # 448 * 2^120 = 1.75 * 2^128
+    layer.t["down"][0, 11, 3] = 0x77        # 240 * 2^120
+    layer.s["down"].view(2, 64, 1)[0, 10:12] = 247
+    w = w * 2.0 ** -10
+    got = layer(x, ids, w, out_dtype=torch.float32)
+    values = fq.mx8_dequantize(layer.t["down"].view(128, 32), layer.s["down"].view(128, 1)).view(2, 64, 32)
+    h = ref.silu(layer.v["gate"][0] @ x.double().cpu().numpy().T) * (layer.v["up"][0] @ x.double().cpu().numpy().T)
+    assert values[0, 10, 3].isinf() and float(values[0, 11, 3]) == 240.0 * 2.0 ** 120
+    for i, h3 in enumerate(h[3]):
+        assert not np.isfinite(float(got[i, 10]))
+        want = 240.0 * 2.0 ** 120 * h3 * float(w[i, 0])
+        if abs(want) < 2.0 ** 117:
+            assert abs(float(got[i, 11]) - want) <= 1e-4 * abs(want)
+    keep = [c for c in range(64) if c not in (10, 11)]
+    assert torch.equal(got[:, keep], clean[:, keep] * 2.0 ** -10)
