@@ -24,9 +24,10 @@
 // holds k = 16 q .. 16 q + 15 of row r: 16 bytes of codes, whose first and last
 // eight are two instructions' operands (of bf16 rows, 8 k's of 32: one).  A code
 // becomes a bf16 exactly (E4M3 and E5M2 have at most 4 significant bits; times a
-// power of two, MXFP8's scale, too).  An fp32 scale is not put into a bf16: it
-// multiplies the chunk's fp32 sums, which it can because a lane's sums are all
-// of weight row r.
+// power of two, MXFP8's scale, too).  An fp32 scale's power of two goes into the
+// bf16s as well, so that sums are in fp32's range where the weights' products
+// are; its significand multiplies the chunk's fp32 sums, which it can because a
+// lane's sums are all of weight row r.
 #include "fp8q_device.h"
 #include "layer_device.h"
 #include "model_launch.h"
@@ -182,24 +183,38 @@ __device__ __forceinline__ u32x4 read_piece(const uint8_t *tile, uint32_t c, uin
   return *reinterpret_cast<const u32x4 *>(tile + (r % R) * kRowBytes + (((c * 4u + q) ^ (r % R)) * 16u));
 }
 
-// Eight codes as bf16 values, times 2^(e8m0 - 127) where they are MXFP8's.
+// Eight codes as bf16 values, times the scale's power of two.
 template <int F>
 __device__ __forceinline__ bf16x8 widen_codes(uint32_t lo, uint32_t hi, float scale) {
   bf16x2 a, b, c, d;
   if constexpr (F == kE5M2) {
-    a = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(lo, 1.0f, false);
-    b = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(lo, 1.0f, true);
-    c = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(hi, 1.0f, false);
-    d = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(hi, 1.0f, true);
+    a = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(lo, scale, false);
+    b = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(lo, scale, true);
+    c = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(hi, scale, false);
+    d = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(hi, scale, true);
   } else {
-    const float s = F == kMx8 ? scale : 1.0f;
-    a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, s, false);
-    b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, s, true);
-    c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, s, false);
-    d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, s, true);
+    a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, false);
+    b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, true);
+    c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, false);
+    d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, true);
   }
   return bf16x8{a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
 }
+
+// An fp32 scale in two factors, both exact: a power of two that leaves every
+// code a normal bf16 (2^-110 to 2^111: E5M2's codes go from 2^-16 to under
+// 2^16), and the rest, the significand of scales in that range.  An infinite or
+// NaN scale's rest is infinite or NaN.
+struct SplitScale {
+  float power, rest;
+
+  __device__ __forceinline__ explicit SplitScale(float scale) {
+    constexpr uint32_t kLeast = 17u << 23, kMost = 238u << 23;
+    const uint32_t e = __float_as_uint(scale) & 0x7F800000u, p = e < kLeast ? kLeast : e > kMost ? kMost : e;
+    power = __uint_as_float(p);
+    rest = scale * __uint_as_float((254u << 23) - p);
+  }
+};
 
 // Sixteen bytes of a token's row (eight k's): an operand.
 __device__ __forceinline__ f32x4 matrix_step(u32x4 a, bf16x8 b, f32x4 d) {
@@ -264,7 +279,7 @@ struct Operand {
   u32x4 v[PARTS][kVectors<F>];
 };
 
-// A piece of weights as operands, and its scale.
+// A piece of weights as operands, and what their products' sum is multiplied by.
 template <int F>
 struct Weights {
   bf16x8 b[kVectors<F>];
@@ -274,8 +289,14 @@ struct Weights {
     if constexpr (F == kBf16) {
       b[0] = __builtin_bit_cast(bf16x8, w);
     } else {
-      b[0] = widen_codes<F>(w.x, w.y, s);
-      b[kVectors<F> - 1] = widen_codes<F>(w.z, w.w, s);
+      float power = s;
+      if constexpr (F != kMx8) {
+        const SplitScale split(s);
+        power = split.power;
+        scale = split.rest;
+      }
+      b[0] = widen_codes<F>(w.x, w.y, power);
+      b[kVectors<F> - 1] = widen_codes<F>(w.z, w.w, power);
     }
   }
 };

@@ -104,7 +104,8 @@ typedef struct {
  * its scale is not rounded), products are summed in fp32, and g, u, h and y
  * are fp32 values; for bf16 output h is held to 15 bits or more, as two bf16
  * numbers.  Values under 2^-126 in magnitude (of x, weights and h) may be taken
- * as zero.
+ * as zero, and MXFP8 values past fp32's range are infinite, as mx8_dequantize
+ * has them.
  * The same expert may be chosen twice by one token.  The same call gives the
  * same bits.  tokens == 0 or hidden == 0 is a successful no-op; with inter == 0
  * out is zeros.

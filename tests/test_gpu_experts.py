@@ -471,3 +471,48 @@ def test_mx8_values_past_fp32_are_infinite(tokens):
             assert abs(float(got[i, 11]) - want) <= 1e-4 * abs(want)
     keep = [c for c in range(64) if c not in (10, 11)]
     assert torch.equal(got[:, keep], clean[:, keep] * 2.0 ** -10)
+
+
+@pytest.mark.parametrize("tokens", [2, 40])
+@pytest.mark.parametrize("width", [64, 200])
+@pytest.mark.parametrize("fmt", FORMATS[1:3])
+def test_scales_far_from_one(fmt, width, tokens):
+    """A power of two taken from x and put into the scales, or from one matrix's
+    scales and put into the next one's, changes no bit: neither code * x nor code
+    * h has to be in fp32's range where code * scale * x is."""
+    experts, dev = 2, require_gpu()
+    x, ids, w = tokens_of(tokens, 1, experts, width, 3)
+    x = torch.where(x < 0, x - 1, x + 1)
+    g = torch.Generator().manual_seed(7)
+
+    def layer(codes, size):
+        made = Layer.__new__(Layer)
+        made.fmt, made.t, made.s = fmt, {}, {}
+        for k in ("gate", "up", "down"):
+            q = codes[torch.randint(0, len(codes), (experts, width, width), generator=g)]
+            q = q | (torch.randint(0, 2, q.shape, generator=g) << 7)
+            made.t[k] = q.to(torch.uint8).to(dev)
+            made.s[k] = (size * (1 + torch.rand(experts * width, -(-width // 128), generator=g))).to(dev)
+        return made
+
+    def times(layer, **powers):
+        made = Layer.__new__(Layer)
+        made.fmt, made.t, made.s = fmt, layer.t, dict(layer.s)
+        for k, p in powers.items():
+            made.s[k] = layer.s[k] * 2.0 ** p
+        return made
+
+    # the largest codes: 448, or 57344 (x times 2^k, h times 2^100 and more)
+    for codes, size, k, p in ((torch.tensor([0x7E, 0x7D] if fmt == E4M3 else [0x7B, 0x7A]), 2.0 ** -5, 120, 100),
+                              # the smallest: 2^-9, or 2^-16
+                              (torch.tensor([1, 2, 3]), 2.0 ** (6 if fmt == E4M3 else 13), -120, -90)):
+        if fmt == E5M2:
+            size, k, p = (2.0 ** -12, 113, 95) if k > 0 else (size, -110, p)
+        made = layer(codes, size)
+        for dtype in (torch.bfloat16, torch.float32):
+            want = made(x, ids, w, out_dtype=dtype)
+            assert want.isfinite().all() and (want != 0).any()
+            moved = times(made, gate=-k, up=-k)
+            assert torch.equal(moved(x * 2.0 ** k, ids, w, out_dtype=dtype), want)
+            moved = times(made, up=p, down=-p)
+            assert torch.equal(moved(x, ids, w, out_dtype=dtype), want)
