@@ -163,7 +163,9 @@ class Items {
   PyObject *list_;
 };
 
-// A list's gradients and, where `scales_at` holds any, their scales.
+// A list's gradients and, where `scales_at` holds any, their scales.  The
+// caller's lists keep the tensors alive, so no Python code may run between this
+// and the call (a number's __float__ could change the lists).
 std::vector<fp8q_grad> gradients(Call &c, int grads_at, int scales_at, int fmt_at) {
   const Items grads(c.object(grads_at), "grads");
   const fp8q_format fmt = format_code(c, fmt_at);
@@ -225,9 +227,9 @@ PyObject *grad_sumsq(PyObject *, PyObject *const *args, Py_ssize_t n) {
 PyObject *grad_clip(PyObject *, PyObject *const *args, Py_ssize_t n) {
   return guarded([&] {
     Call c("fp8q_grad_clip", args, n, 8);
+    const double max_norm = c.number(2, "max_norm"), eps = c.number(5, "eps");
     const std::vector<fp8q_grad> list = gradients(c, 0, 3, 4);
     const at::Tensor &sumsq = c.shaped(1, "sumsq", at::kDouble, {1});
-    const double max_norm = c.number(2, "max_norm"), eps = c.number(5, "eps");
     const at::Tensor norm = c.output(6, "norm_out", at::kFloat, {1});
     const c10::DeviceGuard on(c.device());
     const fp8q_status st =

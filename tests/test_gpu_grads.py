@@ -257,3 +257,21 @@ def test_refusals():
             bad()
     assert torch.equal(t, keep)
     assert float(fq.fp8q_grad_sumsq([t, t])) == 128.0    # reading twice is no harm
+
+
+def test_a_number_that_changes_the_list():
+    """What the lists hold when the tensors are taken is what is clipped."""
+    dev = require_gpu()
+    total = torch.tensor([100.0], dtype=torch.float64, device=dev)
+    kept = torch.ones(1000, device=dev)
+    grads = [kept, torch.ones(5000, device=dev)]
+
+    class Clears:
+        def __float__(self):
+            grads.clear()
+            return 1.0
+
+    assert float(fq.fp8q_grad_clip(grads, total, Clears())) == 10.0
+    grads.append(torch.ones(5000, device=dev))
+    assert float(fq.fp8q_grad_clip(grads, total, 1.0, eps=Clears())) == 10.0
+    assert not grads and bool((kept == 1).all())
