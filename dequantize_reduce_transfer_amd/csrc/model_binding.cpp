@@ -11,6 +11,12 @@
 
 namespace {
 
+// Tells autograd that a call writes to a tensor of the caller's, as torch's own
+// in-place functions do: a graph that has saved it refuses its backward pass.
+void written(c10::TensorImpl *t) {
+  if (!t->is_inference()) t->bump_version();
+}
+
 fp8q_logits_dtype logits_code(at::ScalarType t) { return t == at::kFloat ? FP8Q_LOGITS_F32 : FP8Q_LOGITS_BF16; }
 
 void check_route(const at::Tensor &logits, long long topk) {
@@ -57,6 +63,7 @@ PyObject *moe_route_backward(PyObject *, PyObject *const *args, Py_ssize_t n) {
     const fp8q_status st = fp8q_moe_route_backward(
         f32(dweights), ptr(logits), logits_code(logits.scalar_type()), f32(weights), i32(ids), logits.size(0),
         (int)logits.size(1), (int)dweights.size(1), normalize, ptr(dlogits), c.stream(6));
+    if (st == FP8Q_OK && !c.absent(5)) written(dlogits.unsafeGetTensorImpl());
     return result(st, {dlogits});
   });
 }
@@ -163,10 +170,12 @@ class Items {
   PyObject *list_;
 };
 
-// A list's gradients and, where `scales_at` holds any, their scales.  The
-// caller's lists keep the tensors alive, so no Python code may run between this
-// and the call (a number's __float__ could change the lists).
-std::vector<fp8q_grad> gradients(Call &c, int grads_at, int scales_at, int fmt_at) {
+// A list's gradients and, where `scales_at` holds any, their scales; and, where
+// wanted, the tensors that clipping writes.  The caller's lists keep the tensors
+// alive, so no Python code may run between this and the call (a number's
+// __float__ could change the lists).
+std::vector<fp8q_grad> gradients(Call &c, int grads_at, int scales_at, int fmt_at,
+                                 std::vector<c10::TensorImpl *> *clipped = nullptr) {
   const Items grads(c.object(grads_at), "grads");
   const fp8q_format fmt = format_code(c, fmt_at);
   PyObject *none = Py_None;
@@ -174,6 +183,7 @@ std::vector<fp8q_grad> gradients(Call &c, int grads_at, int scales_at, int fmt_a
   const Items *given = nullptr;
   std::vector<fp8q_grad> list;
   list.reserve((size_t)grads.size());
+  if (clipped) clipped->reserve((size_t)grads.size());
   const auto fill = [&] {
     for (Py_ssize_t i = 0; i < grads.size(); ++i) {
       const at::Tensor &t = c.tensor(grads[i], "a gradient", {at::kFloat, at::kBFloat16, at::kByte}, true);
@@ -192,7 +202,9 @@ std::vector<fp8q_grad> gradients(Call &c, int grads_at, int scales_at, int fmt_a
           refuse("a gradient's scales must be one per 128 codes, or one");
         g.scales = f32(s);
         g.scale_count = (size_t)s.numel();
+        if (clipped) clipped->push_back(s.unsafeGetTensorImpl());
       }
+      if (clipped && scale == none) clipped->push_back(t.unsafeGetTensorImpl());
       list.push_back(g);
     }
   };
@@ -228,13 +240,16 @@ PyObject *grad_clip(PyObject *, PyObject *const *args, Py_ssize_t n) {
   return guarded([&] {
     Call c("fp8q_grad_clip", args, n, 8);
     const double max_norm = c.number(2, "max_norm"), eps = c.number(5, "eps");
-    const std::vector<fp8q_grad> list = gradients(c, 0, 3, 4);
+    std::vector<c10::TensorImpl *> clipped;
+    const std::vector<fp8q_grad> list = gradients(c, 0, 3, 4, &clipped);
     const at::Tensor &sumsq = c.shaped(1, "sumsq", at::kDouble, {1});
     const at::Tensor norm = c.output(6, "norm_out", at::kFloat, {1});
     const c10::DeviceGuard on(c.device());
     const fp8q_status st =
         fp8q_grad_clip(list.data(), list.size(), static_cast<const double *>(ptr(sumsq)), max_norm, eps,
                        f32(norm), c.stream(7));
+    if (st == FP8Q_OK)
+      for (c10::TensorImpl *t : clipped) written(t);
     return result(st, {norm});
   });
 }

@@ -120,7 +120,7 @@ def fp8q_moe_route_backward(dweights: torch.Tensor, logits: torch.Tensor, weight
     dweights: gradient of the weights (fp32 [tokens, topk]); logits, weights and
     ids as in the forward pass, whose ``normalize`` it takes too.  Entries whose
     id is outside the experts are left out.  ``dlogits_out`` may be ``logits``
-    itself.
+    itself, and is changed in place to autograd.
     """
     if stream is not None:
         return _on_stream(stream, "fp8q_moe_route_backward", fp8q_moe_route_backward, dweights, logits, weights,
@@ -195,7 +195,8 @@ def fp8q_grad_clip(grads: Sequence[torch.Tensor], sumsq: torch.Tensor, max_norm:
     sumsq fp64 [1], of the whole gradient.  Every gradient is multiplied by
     ``min(1, max_norm / (sqrt(sumsq) + eps))``; of codes, their scales are, and
     the codes stay.  Nothing is written where that is 1.  A NaN norm makes them
-    all NaN.
+    all NaN.  To autograd the call is an in-place change of them (codes: of their
+    scales), whatever the norm: a graph that has saved one refuses its backward.
     """
     if stream is not None:
         return _on_stream(stream, "fp8q_grad_clip", fp8q_grad_clip, grads, sumsq, max_norm, scales, fmt, eps,

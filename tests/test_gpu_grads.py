@@ -259,6 +259,34 @@ def test_refusals():
     assert float(fq.fp8q_grad_sumsq([t, t])) == 128.0    # reading twice is no harm
 
 
+def test_clipping_is_an_in_place_change_to_autograd():
+    dev = require_gpu()
+    total = torch.tensor([100.0], dtype=torch.float64, device=dev)
+    x = torch.arange(1.0, 5.0, device=dev, requires_grad=True)
+    g, = torch.autograd.grad((x ** 3).sum(), x, create_graph=True)
+    penalty = (g * g).sum()                 # saves g
+    fq.fp8q_grad_clip([g.detach()], total, 1.0)
+    with pytest.raises(RuntimeError, match="inplace"):
+        penalty.backward()
+    q, s = torch.zeros(300, dtype=torch.uint8, device=dev), torch.ones(3, device=dev)
+    t, b = torch.ones(7, device=dev), torch.ones(9, dtype=torch.bfloat16, device=dev)
+    before = [v._version for v in (t, q, s, b)]
+    fq.fp8q_grad_clip([t, q, b], total, 1.0, scales=[None, s, None])
+    assert [v._version - n for v, n in zip((t, q, s, b), before)] == [1, 0, 1, 1]
+    fq.fp8q_grad_clip((t,), total, 1.0, stream=torch.cuda.Stream(dev))
+    torch.cuda.synchronize()
+    assert t._version == before[0] + 2
+    fq.fp8q_grad_sumsq([t, q, b], scales=[None, s, None])
+    with pytest.raises(fq.Fp8qError):
+        fq.fp8q_grad_clip([t], total, -1.0)
+    assert t._version == before[0] + 2
+    with torch.inference_mode():
+        i = torch.ones(5, device=dev)
+        fq.fp8q_grad_clip([i], total, 1.0, eps=0.0)
+    fq.fp8q_grad_clip([i], total, 1.0, eps=0.0)
+    assert bool((i == torch.full((5,), 0.1, device=dev) * torch.tensor(0.1)).all())
+
+
 def test_a_number_that_changes_the_list():
     """What the lists hold when the tensors are taken is what is clipped."""
     dev = require_gpu()

@@ -193,3 +193,19 @@ def test_refusals():
             bad()
     with pytest.raises(fq.Fp8qError):
         fq.fp8q_moe_route(l, 2, weights_out=l.view(-1)[:8].view(4, 2))
+
+
+@pytest.mark.parametrize("normalize", [True, False])
+def test_gradients_in_the_logits_place_are_a_change_to_autograd(normalize):
+    dev = require_gpu()
+    x = torch.randn(6, 8, device=dev, requires_grad=True)
+    logits = x * 2.0
+    loss = (logits * logits).sum()          # saves the logits
+    weights, ids = fq.fp8q_moe_route(logits.detach(), 2, normalize=normalize)
+    want = fq.fp8q_moe_route_backward(torch.ones_like(weights), logits.detach(), weights, ids, normalize=normalize)
+    version = logits._version
+    got = fq.fp8q_moe_route_backward(torch.ones_like(weights), logits.detach(), weights, ids, normalize=normalize,
+                                     dlogits_out=logits.detach())
+    assert torch.equal(got, want) and logits._version == version + 1
+    with pytest.raises(RuntimeError, match="inplace"):
+        loss.backward()
