@@ -82,9 +82,11 @@ FP8Q_API fp8q_status fp8q_moe_route_backward(const float *dweights, const void *
 
 /*
  * One matrix of every expert: expert e's rows [r, width] are rows
- * [e * expert_rows, e * expert_rows + r) of one array of rows, as the codec
- * quantizes them (fp8q_row_format: bf16, codes with fp32 scales per 128 of a
- * row, or MXFP8).  expert_rows >= r: gate and up may be the two halves of one
+ * [e * expert_rows, e * expert_rows + r) of one array of rows in a
+ * fp8q_row_format: bf16, codes with ceil(width / 128) fp32 scales a row, or
+ * MXFP8.  mx8_quantize leaves matrices so, and fp8q_quantize those whose width
+ * is a multiple of 128 (its blocks run on from row to row; others are quantized
+ * a row at a time).  expert_rows >= r: gate and up may be the two halves of one
  * [experts, 2 * inter, hidden] array.  Codes need no alignment, bf16 rows 2
  * bytes, fp32 scales 4.
  */
@@ -105,7 +107,9 @@ typedef struct {
  * are fp32 values; for bf16 output h is held to 15 bits or more, as two bf16
  * numbers.  Values under 2^-126 in magnitude (of x, weights and h) may be taken
  * as zero, and MXFP8 values past fp32's range are infinite, as mx8_dequantize
- * has them.
+ * has them.  An infinite fp32 scale makes the g, u or y that it is part of
+ * infinite or NaN: it multiplies the sum of 64 of its block's products, where
+ * code * scale summed one by one would be NaN for codes of both signs.
  * The same expert may be chosen twice by one token.  The same call gives the
  * same bits.  tokens == 0 or hidden == 0 is a successful no-op; with inter == 0
  * out is zeros.
@@ -170,9 +174,10 @@ FP8Q_API fp8q_status fp8q_grad_sumsq(const fp8q_grad *grads, size_t n, double *s
 /*
  * Clips gradients to a largest global norm, in place: with
  *   norm = sqrt(sumsq),   c = min(1, max_norm / (norm + eps))   (in fp64)
- * every value is multiplied by c (fp32, rounded once to its type); of codes
- * the scales are, and the codes stay.  With c == 1 nothing is written.  A NaN
- * norm makes all of them NaN (codes: their scales); an infinite one makes
+ * every value is multiplied by c, rounded to fp32, in fp32, and rounded once to
+ * its type; of codes the scales are, and the codes stay.  With c == 1 nothing is
+ * written.  A NaN norm makes all of them NaN (codes: their scales), as 0 / 0 does
+ * (eps, max_norm and the norm all 0); an infinite one makes
  * finite values 0 and infinite ones NaN; unless max_norm is infinite: then
  * nothing is ever written.
  *   grads      n structs in host memory, none overlapping another
