@@ -11,9 +11,9 @@
 //
 // The rows of the experts that a token chose are read once, and little else is:
 // at 8 of 128 experts of 2048 x 768 a token's MXFP8 rows are 39 MB, so HBM
-// bounds all of them for as long as an expert has few tokens.  The rows come in
-// non-temporally, which took 10% off 32 tokens (119 us to 107) and left one token
-// where it was.  Measured on MI355X, whole calls: that layer in MXFP8, one token
+// bounds all of them for as long as an expert has few tokens.  Rows that go
+// straight into LDS (TileLoad) come in non-temporally, which took 10% off 32
+// tokens (119 us to 107) and left one token where it was.  Measured on MI355X, whole calls: that layer in MXFP8, one token
 // 17 us (its bytes at 6.5 TB/s: 6), 2 26 (12), 5 42 (26), 32 99 to 104 (84),
 // 128 130 (96); 128 tokens through 2 of 8 experts of 4096 x 14336 in bf16 504 to
 // 519 (434).
@@ -39,13 +39,12 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 enum RowFormat : int { kBf16 = 0, kE4M3 = 1, kE5M2 = 2, kMx8 = 3 };   // fp8q_row_format
 
-constexpr uint32_t kMaxPairs = 1024;     // FP8Q_EXPERTS_MAX_PAIRS
 constexpr int kGateUpWaves = 4;          // of a gate_up workgroup: they share the k's
 constexpr int kDownWaves = 8;            // of a down workgroup: they share the experts
 // Pairs up to which one kernel multiplies by down and adds up.  At 8 of 128
-// experts of 2048 x 768, 16 pairs take 26 us this way and 31 the other, which is
-// a launch more; 32 pairs take 41 and 36, since a workgroup's waves walk over
-// four experts each here.
+// experts of 2048 x 768 in MXFP8, 16 pairs take 27 us this way and 32 the other,
+// which is a launch more; 24 pairs 38 and 34 (in bf16 49 and 50), 32 pairs 44 and
+// 36 (58 and 58), since a workgroup's waves walk over four experts each here.
 constexpr uint32_t kFewPairs = 24;
 
 // The experts of pairs p[0 .. N), -1 where they have none (an id outside the
@@ -990,8 +989,11 @@ hipError_t down(const Layer &a, int wide, hipStream_t stream) {
 
 // 0: few pairs; else how many times 16 tokens the wide kernels hold, which have
 // to be few for an expert's share of the pairs, since room for more takes LDS and
-// registers from the loads: at 8 pairs an expert 16 take 156 us, 32 168 and 64
-// 204; at 32 pairs (wide bf16 experts) 16 take 1339, 32 859 and 64 639.
+// registers from the loads: at 8 pairs an expert 16 take 134 us, 32 138 and 64
+// 171; at 16 pairs of wide MXFP8 experts 419, 294 and 345; at 32 (bf16) 1229, 795
+// and 551.  The share is pairs / experts, which the host knows; where few experts
+// have most of the pairs it is too low (64 tokens that all choose the same 8 of
+// 128: 151 us, and 71 if 64 were held).
 int wide_of(uint32_t pairs, uint32_t experts) {
   if (pairs <= kFewPairs) return 0;
   const uint32_t each = (pairs + experts - 1) / experts;
