@@ -16,7 +16,7 @@
 // tokens (119 us to 107) and left one token where it was.  Measured on MI355X, whole calls: that layer in MXFP8, one token
 // 17 us (its bytes at 6.5 TB/s: 6), 2 26 (12), 5 42 (26), 32 99 to 104 (84),
 // 128 130 (96); 128 tokens through 2 of 8 experts of 4096 x 14336 in bf16 504 to
-// 519 (434).
+// 525 (434).
 //
 // Products are 16x16x32 bf16 matrix instructions: the tokens' rows are operand
 // A, 16 weight rows operand B, and both may take the k's of a chunk of 64 in
@@ -127,7 +127,7 @@ __device__ __forceinline__ u32x4 load_up_to(const uint8_t *row, uint32_t at, uin
 //   DIRECT  rows and their length are multiples of 16 bytes: straight into LDS;
 //           otherwise through registers, which `commit` writes to LDS, so that
 //           several tiles' loads may be on their way together (78 choices
-//           among 60 E4M3 experts of 1411 x 1000: 72 us, 2.3 TB/s)
+//           among 60 E4M3 experts of 1411 x 1000: 74 us, 2.2 TB/s)
 template <int R, bool DIRECT>
 struct TileLoad {
   u32x4 v[DIRECT ? 1 : R / 4];
