@@ -13,10 +13,10 @@
 // at 8 of 128 experts of 2048 x 768 a token's MXFP8 rows are 39 MB, so HBM
 // bounds all of them for as long as an expert has few tokens.  Rows that go
 // straight into LDS (TileLoad) come in non-temporally, which took 10% off 32
-// tokens (119 us to 107) and left one token where it was.  Measured on MI355X, whole calls: that layer in MXFP8, one token
-// 17 us (its bytes at 6.5 TB/s: 6), 2 26 (12), 5 42 (26), 32 99 to 104 (84),
-// 128 130 (96); 128 tokens through 2 of 8 experts of 4096 x 14336 in bf16 504 to
-// 525 (434).
+// tokens (119 us to 107) and left one token where it was.  Measured on MI355X,
+// whole calls: that layer in MXFP8, one token 17 us (its bytes at 6.5 TB/s: 6), 2
+// 26 (12), 5 42 (26), 32 99 to 104 (84), 128 130 (96); 128 tokens through 2 of 8
+// experts of 4096 x 14336 in bf16 504 to 525 (434).
 //
 // Products are 16x16x32 bf16 matrix instructions: the tokens' rows are operand
 // A, 16 weight rows operand B, and both may take the k's of a chunk of 64 in

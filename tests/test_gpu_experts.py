@@ -516,3 +516,16 @@ def test_scales_far_from_one(fmt, width, tokens):
             assert torch.equal(moved(x * 2.0 ** k, ids, w, out_dtype=dtype), want)
             moved = times(made, up=p, down=-p)
             assert torch.equal(moved(x, ids, w, out_dtype=dtype), want)
+
+
+@pytest.mark.parametrize("tokens", [2, 40])
+@pytest.mark.parametrize("fmt", FORMATS[1:3])
+def test_subnormal_scales(fmt, tokens):
+    layer = Layer(fmt, 2, 96, 200, 1)
+    x, ids, w = tokens_of(tokens, 1, 2, 96, 3)
+    layer.s["down"].fill_(2.0 ** -30)
+    want = layer(x, ids, w, out_dtype=torch.float32)
+    layer.s["up"] *= 2.0 ** 110
+    layer.s["down"].fill_(2.0 ** -140)
+    got = layer(x, ids, w, out_dtype=torch.float32)
+    assert bool((want != 0).any()) and torch.equal(got, want)
